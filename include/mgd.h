@@ -408,6 +408,116 @@ mgd_status mgd_spec_sample_noalloc(const float *target_logits, const float *draf
                                    int mode, int row, int32_t *out_tokens, int32_t *num_accepted,
                                    void *stream);
 
+/* ------------------------------------------------------------------------ *
+ * Attention for a batch that shares a long prefix (a system prompt, a common
+ * document): every sequence attends to the same prefix rows, held once, and to
+ * its own cache behind them.  [MagicDec] section 3.2 is about the bytes of the
+ * KV cache a verify pass reads; here the shared part of them is read once for
+ * the whole batch.  The papers have no counterpart to this call; it is verify
+ * attention (T = 1: draft attention) over the concatenation.
+ *
+ *   q         [B, T, Hq, D]                  in_dtype, contiguous
+ *   k_prefix, v_prefix [Hkv, prefix_cap, D]  in_dtype; element (h, j, d) at
+ *                                            h*prefix_head_stride + j*D + d
+ *   prefix_len [1] int32 (device)            rows of the prefix, 0 <= prefix_len <= prefix_cap
+ *   k, v, kv_len                             each sequence's own rows, as for mgd_verify_attn
+ *                                            (T <= kv_len[b] <= kv_cap, the T rows included)
+ *   out, lse                                 as for mgd_verify_attn
+ *
+ * Row t of sequence b attends to every prefix row and to own rows
+ * 0 .. kv_len[b]-T+t; scores are sm_scale * <q, k>; softmax and accumulation in
+ * float32.
+ * A prefix_len out of range leaves every output unspecified, a kv_len out of
+ * range that sequence's (MGD_DEVERR_KV_LEN).
+ * Supported: D in {64, 128}; 1 <= T <= 17; Hq % Hkv == 0; fewer than 2^31 rows
+ * B * T * Hq.
+ * ------------------------------------------------------------------------ */
+size_t mgd_prefix_workspace_size(int B, int T, int Hq, int Hkv, int D, int prefix_cap, int kv_cap);
+mgd_status mgd_prefix_attn(const void *q, const void *k_prefix, const void *v_prefix, const int32_t *prefix_len,
+                           int prefix_cap, int64_t prefix_head_stride, const void *k, const void *v,
+                           const int32_t *kv_len, int B, int T, int Hq, int Hkv, int D, int kv_cap,
+                           int64_t kv_batch_stride, int64_t kv_head_stride, float sm_scale, mgd_dtype in_dtype,
+                           void *out, mgd_dtype out_dtype, float *lse, void *ws, size_t ws_bytes, void *stream);
+
+/* ------------------------------------------------------------------------ *
+ * Rotary positions of new rows, and their append to the cache.  The attention
+ * calls read K rows that carry their position already; this call makes them:
+ * it turns the new rows of q and k by their positions, writes q to q_out and
+ * appends k and v to the cache.
+ *
+ *   q [B, T, Hq, D], k_new, v_new [B, T, Hkv, D]  dtype; the heads of one token
+ *             are packed, tokens are *_token_stride elements apart (views of one
+ *             fused projection are taken as they are)
+ *   turns     [rotary_dim / 2] uint64 (device), magnitude: from mgd_rope_frequencies
+ *   kv_len    [B] int32 (device): rows of sequence b, INCLUDING the new ones
+ *   new_len   [B] int32 (device) or NULL (T new rows each): sequence b has
+ *             n_b = new_len[b] new rows, the first n_b of its T; 0 <= n_b <= T
+ *   pos_offset int32 (device) or NULL (0): sequence b's positions start at
+ *             pos_offset[b * pos_offset_stride] (stride 0: one offset for all,
+ *             e.g. the length of a shared prefix)
+ *   q_out     [B, T, Hq, D] dtype, contiguous (may be q itself when q is)
+ *   k, v      [B, Hkv, kv_cap, D] dtype, strides as for mgd_verify_attn
+ *
+ * New row t < n_b goes to cache row kv_len[b] - n_b + t; its position is that
+ * row plus the offset.  Elements i and i + rotary_dim/2 of a head (interleaved
+ * == 0) or 2i and 2i + 1 (interleaved != 0) turn together by position times
+ * frequency i; elements from rotary_dim on are copied.  Rows t >= n_b of q_out
+ * and every other cache row are left as they were.  cos and sin in float32 of
+ * the exact angle modulo one turn (positions up to 2^31), results rounded once.
+ * A sequence with new_len or kv_len out of range (0 <= n_b <= T, n_b <= kv_len
+ * <= kv_cap) is left untouched and flagged (MGD_DEVERR_KV_LEN).
+ * Supported: rows of D elements a multiple of 16 bytes; rotary_dim even and in
+ * [2, D]; token strides multiples of 16 bytes.
+ * ------------------------------------------------------------------------ */
+typedef enum {
+  MGD_ROPE_PLAIN = 0,  /* base^(-2i/rotary_dim) */
+  MGD_ROPE_LINEAR = 1, /* positions divided by p[0] = factor */
+  MGD_ROPE_NTK = 2,    /* base * factor^(rotary_dim/(rotary_dim-2)); p[0] = factor */
+  MGD_ROPE_LLAMA3 = 3, /* p = factor, low_freq_factor, high_freq_factor, original length: waves longer than
+                          original / low are slowed by factor, shorter than original / high kept, a linear
+                          ramp in turns over the original length between */
+  MGD_ROPE_YARN = 4    /* p = factor, beta_fast, beta_slow, original length: pairs that turn more than
+                          beta_fast times over the original length kept, fewer than beta_slow slowed by
+                          factor, a linear ramp in the pair's index between; magnitude 0.1 ln(factor) + 1 */
+} mgd_rope_scaling;
+/* Host only: fills turns[rotary_dim / 2] and *magnitude in host memory, to be copied to the device once.
+ * `params` may be NULL for MGD_ROPE_PLAIN.  Errors: MGD_ERR_INVALID_ARG. */
+mgd_status mgd_rope_frequencies(int rotary_dim, double base, int scaling, const double *params, uint64_t *turns,
+                                float *magnitude);
+size_t mgd_rope_workspace_size(int B);
+mgd_status mgd_rope_append(const void *q, int64_t q_token_stride, const void *k_new, int64_t k_token_stride,
+                           const void *v_new, int64_t v_token_stride, const uint64_t *turns, float magnitude,
+                           int rotary_dim, int interleaved, int B, int T, int Hq, int Hkv, int D, mgd_dtype dtype,
+                           const int32_t *kv_len, const int32_t *new_len, const int32_t *pos_offset,
+                           int pos_offset_stride, void *q_out, void *k, void *v, int kv_cap,
+                           int64_t kv_batch_stride, int64_t kv_head_stride, void *ws, size_t ws_bytes, void *stream);
+
+/* ------------------------------------------------------------------------ *
+ * Log probabilities of given tokens (e.g. a round's out_tokens under its target
+ * logits), with the entropy of each distribution, the token's rank and the most
+ * likely alternatives.
+ *
+ *   logits    [R, V] dtype (MGD_F32 or MGD_BF16), rows row_stride elements apart
+ *   tokens    [R] int32: the token of each row; -1 (padding) skips the row
+ *   logprob   [R] float32: log softmax(x)[token];  entropy [R] float32, in nats
+ *   rank      [R] int32: entries ordered before the token (0: the most likely)
+ *   top_ids   [R, K] int32, top_logprobs [R, K] float32: the first K entries
+ *             (may be NULL when K == 0)
+ *
+ * The order is value descending, then index ascending.  Entries that are -inf
+ * have no place among the alternatives: what is left of the K is -1 and -inf.  A
+ * skipped row gets logprob 0, entropy 0, rank -1 and no alternatives.  A row
+ * that holds a NaN or +inf, or nothing but -inf, has no distribution: logprob
+ * and entropy NaN, rank -1, no alternatives.  Sums in float32.  A token outside
+ * [-1, V) is treated as -1 and flagged (MGD_DEVERR_TOKEN).
+ * Supported: 1 <= V < 2^31; 0 <= K <= 32; row_stride >= V; any alignment of
+ * the element type.
+ * ------------------------------------------------------------------------ */
+size_t mgd_logprobs_workspace_size(int R, int V, int K);
+mgd_status mgd_token_logprobs(const void *logits, int64_t row_stride, mgd_dtype dtype, const int32_t *tokens, int R,
+                              int V, int K, float *logprob, float *entropy, int32_t *rank, int32_t *top_ids,
+                              float *top_logprobs, void *ws, size_t ws_bytes, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -5,7 +5,9 @@
 #include <cuda_runtime.h>
 #include <nvtx3/nvToolsExt.h>
 
+#include <algorithm>
 #include <atomic>
+#include <cmath>
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
@@ -478,6 +480,236 @@ mgd_status mgd_commit_round(const int32_t *num_accepted, int B, int gamma, int H
                                 kv_head_stride, k_draft, v_draft, draft_cap, draft_batch_stride, draft_head_stride,
                                 draft_len, ws, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? ok() : cuda_fail(e, "commit launch");
+}
+
+size_t mgd_prefix_workspace_size(int B, int T, int Hq, int Hkv, int D, int prefix_cap, int kv_cap) {
+  if (B <= 0 || T < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv || D < 1 || prefix_cap < 1 || kv_cap < 1 ||
+      static_cast<int64_t>(B) * T * Hq > INT32_MAX)
+    return kAlign;
+  const int sms = current_sm_count();
+  return std::max(plan_prefix(B, T, Hq, Hkv, D, prefix_cap, kv_cap, 0, sms).ws_bytes,
+                  plan_prefix(B, T, Hq, Hkv, D, prefix_cap, kv_cap, 1, sms).ws_bytes);
+}
+
+mgd_status mgd_prefix_attn(const void *q, const void *k_prefix, const void *v_prefix, const int32_t *prefix_len,
+                           int prefix_cap, int64_t prefix_head_stride, const void *k, const void *v,
+                           const int32_t *kv_len, int B, int T, int Hq, int Hkv, int D, int kv_cap,
+                           int64_t kv_batch_stride, int64_t kv_head_stride, float sm_scale, mgd_dtype in_dtype,
+                           void *out, mgd_dtype out_dtype, float *lse, void *ws, size_t ws_bytes, void *stream) {
+  const NvtxRange nvtx_range("mgd_prefix_attn");
+  mgd_status s = check_attention(q, k, v, kv_len, B, T, Hq, Hkv, D, kv_cap, kv_batch_stride, kv_head_stride, in_dtype,
+                                 out, out_dtype, ws);
+  if (s != MGD_OK) return s;
+  if (prefix_cap < 1) return fail(MGD_ERR_INVALID_ARG, "prefix capacity must be >= 1 (got %d)", prefix_cap);
+  if (prefix_head_stride < static_cast<int64_t>(prefix_cap) * D)
+    return fail(MGD_ERR_INVALID_ARG, "prefix_head_stride %lld < capacity * D",
+                static_cast<long long>(prefix_head_stride));
+  if (B == 0) return ok();
+  if (!k_prefix || !v_prefix || !prefix_len) return fail(MGD_ERR_INVALID_ARG, "null pointer argument");
+  const int esz = (in_dtype == MGD_F32) ? 4 : 2;
+  if (!aligned16(k_prefix) || !aligned16(v_prefix) || (prefix_head_stride * esz) % 16 != 0)
+    return fail(MGD_ERR_INVALID_ARG, "k_prefix, v_prefix and the prefix stride must be 16-byte aligned");
+  if (static_cast<int64_t>(B) * T * Hq > INT32_MAX)
+    return fail(MGD_ERR_UNSUPPORTED, "B * T * Hq must be below 2^31");
+  const int in_f32 = in_dtype == MGD_F32;
+  const PrefixPlan plan = plan_prefix(B, T, Hq, Hkv, D, prefix_cap, kv_cap, in_f32, current_sm_count());
+  if (ws_bytes < plan.ws_bytes) return fail(MGD_ERR_WORKSPACE, "workspace %zu < %zu bytes", ws_bytes, plan.ws_bytes);
+  if (static_cast<int64_t>(plan.g.RT) * Hkv * ((prefix_cap + plan.g.key_tile - 1) / plan.g.key_tile) > INT32_MAX)
+    return fail(MGD_ERR_UNSUPPORTED, "too many rows and prefix keys for one call");
+  PrefixArgs a;
+  a.q = q;
+  a.k = k_prefix;
+  a.v = v_prefix;
+  a.prefix_len = prefix_len;
+  a.head_stride = prefix_head_stride;
+  a.sm_scale = sm_scale;
+  a.out = out;
+  a.out_bf16 = (out_dtype == MGD_BF16);
+  a.lse = lse;
+  a.ws = ws;
+  a.stream = static_cast<cudaStream_t>(stream);
+  unsigned char *w = static_cast<unsigned char *>(ws);
+  auto own = [&] {
+    return run_attention(q, k, v, kv_len, B, T, Hq, Hkv, D, kv_cap, kv_batch_stride, kv_head_stride, sm_scale, in_dtype,
+                         w + plan.off_own_o, MGD_F32, reinterpret_cast<float *>(w + plan.off_own_l), ws, ws_bytes,
+                         stream);
+  };
+  // The float32 attention clears the header ahead of its launch, so the prefix kernel raises its
+  // bits after it; the bf16 one closes the call's error word, so there the prefix goes first.
+  if (in_f32 && (s = own()) != MGD_OK) return s;
+  cudaError_t e = launch_prefix_simt(plan, a, in_f32);
+  if (e != cudaSuccess) return cuda_fail(e, "prefix attention launch");
+  if (!in_f32 && (s = own()) != MGD_OK) return s;
+  e = launch_prefix_merge(plan, a);
+  return e == cudaSuccess ? ok() : cuda_fail(e, "prefix merge launch");
+}
+
+mgd_status mgd_rope_frequencies(int rotary_dim, double base, int scaling, const double *params, uint64_t *turns,
+                                float *magnitude) {
+  if (rotary_dim < 2 || rotary_dim % 2) return fail(MGD_ERR_INVALID_ARG, "rotary_dim must be even and >= 2 (got %d)", rotary_dim);
+  if (!(base > 1.0) || !std::isfinite(base)) return fail(MGD_ERR_INVALID_ARG, "base must be finite and above 1");
+  if (scaling < MGD_ROPE_PLAIN || scaling > MGD_ROPE_YARN) return fail(MGD_ERR_INVALID_ARG, "bad scaling %d", scaling);
+  if (!turns || !magnitude || (scaling != MGD_ROPE_PLAIN && !params)) return fail(MGD_ERR_INVALID_ARG, "null pointer argument");
+  const double two_pi = 6.283185307179586476925;
+  double factor = 1.0, a = 0.0, b = 0.0, original = 0.0;
+  if (scaling != MGD_ROPE_PLAIN) {
+    factor = params[0];
+    if (!(factor >= 1.0) || !std::isfinite(factor)) return fail(MGD_ERR_INVALID_ARG, "factor must be finite and >= 1");
+  }
+  if (scaling == MGD_ROPE_NTK) {
+    if (rotary_dim < 4) return fail(MGD_ERR_INVALID_ARG, "this scaling needs rotary_dim >= 4");
+    base *= std::pow(factor, static_cast<double>(rotary_dim) / (rotary_dim - 2));
+  }
+  if (scaling == MGD_ROPE_LLAMA3 || scaling == MGD_ROPE_YARN) {
+    a = params[1];
+    b = params[2];
+    original = params[3];
+    const bool up = scaling == MGD_ROPE_LLAMA3 ? a < b : b < a;
+    if (!(a > 0.0) || !(b > 0.0) || !up || !std::isfinite(a) || !std::isfinite(b) || !(original >= 1.0) ||
+        !std::isfinite(original))
+      return fail(MGD_ERR_INVALID_ARG, "the scaling's two bounds must be positive and in order, the original length >= 1");
+  }
+  double lo = 0.0, hi = 0.0;
+  if (scaling == MGD_ROPE_YARN) {
+    // index of the pair that makes `t` turns over the original length
+    auto index = [&](double t) { return rotary_dim * std::log(original / (t * two_pi)) / (2.0 * std::log(base)); };
+    lo = std::max(std::floor(index(a)), 0.0);
+    hi = std::min(std::ceil(index(b)), static_cast<double>(rotary_dim - 1));
+  }
+  for (int i = 0; i < rotary_dim / 2; ++i) {
+    double f = std::pow(base, -2.0 * i / rotary_dim);  // radians per position
+    if (scaling == MGD_ROPE_LINEAR) f /= factor;
+    if (scaling == MGD_ROPE_LLAMA3) {
+      const double keep = std::min(std::max((original * f / two_pi - a) / (b - a), 0.0), 1.0);
+      f *= keep + (1.0 - keep) / factor;
+    }
+    if (scaling == MGD_ROPE_YARN) {
+      const double slow = std::min(std::max((i - lo) / std::max(hi - lo, 1e-3), 0.0), 1.0);
+      f = f * (1.0 - slow) + f / factor * slow;
+    }
+    turns[i] = static_cast<uint64_t>(std::ldexp(f / two_pi, 64));  // f <= 1: below 2^62
+  }
+  *magnitude = scaling == MGD_ROPE_YARN ? static_cast<float>(0.1 * std::log(factor) + 1.0) : 1.f;
+  return ok();
+}
+
+size_t mgd_rope_workspace_size(int B) {
+  (void)B;
+  return kAlign;
+}
+
+mgd_status mgd_rope_append(const void *q, int64_t q_token_stride, const void *k_new, int64_t k_token_stride,
+                           const void *v_new, int64_t v_token_stride, const uint64_t *turns, float magnitude,
+                           int rotary_dim, int interleaved, int B, int T, int Hq, int Hkv, int D, mgd_dtype dtype,
+                           const int32_t *kv_len, const int32_t *new_len, const int32_t *pos_offset,
+                           int pos_offset_stride, void *q_out, void *k, void *v, int kv_cap, int64_t kv_batch_stride,
+                           int64_t kv_head_stride, void *ws, size_t ws_bytes, void *stream) {
+  const NvtxRange nvtx_range("mgd_rope_append");
+  if (B < 0) return fail(MGD_ERR_INVALID_ARG, "B must be >= 0 (got %d)", B);
+  if (T < 1 || Hq < 1 || Hkv < 1 || D < 1 || kv_cap < 1)
+    return fail(MGD_ERR_INVALID_ARG, "need T, Hq, Hkv, D, kv_cap >= 1");
+  if (dtype != MGD_BF16 && dtype != MGD_F32) return fail(MGD_ERR_INVALID_ARG, "bad dtype %d", dtype);
+  const int esz = (dtype == MGD_F32) ? 4 : 2;
+  if ((static_cast<int64_t>(D) * esz) % 16 != 0) return fail(MGD_ERR_UNSUPPORTED, "rows must be a multiple of 16 bytes");
+  if (rotary_dim < 2 || rotary_dim > D || rotary_dim % 2)
+    return fail(MGD_ERR_INVALID_ARG, "rotary_dim must be even and in [2, D] (got %d)", rotary_dim);
+  if (rotary_dim > 2048) return fail(MGD_ERR_UNSUPPORTED, "rotary_dim must be at most 2048 (got %d)", rotary_dim);
+  if (static_cast<int64_t>(B) * T > INT32_MAX) return fail(MGD_ERR_UNSUPPORTED, "B * T must be below 2^31");
+  if ((static_cast<int64_t>(Hq) + 2 * static_cast<int64_t>(Hkv)) * D > INT32_MAX)
+    return fail(MGD_ERR_UNSUPPORTED, "(Hq + 2 Hkv) * D must be below 2^31");
+  if (q_token_stride < static_cast<int64_t>(Hq) * D || k_token_stride < static_cast<int64_t>(Hkv) * D ||
+      v_token_stride < static_cast<int64_t>(Hkv) * D)
+    return fail(MGD_ERR_INVALID_ARG, "token strides smaller than a token's heads");
+  if (kv_head_stride < static_cast<int64_t>(kv_cap) * D || kv_batch_stride < kv_head_stride * Hkv)
+    return fail(MGD_ERR_INVALID_ARG, "strides smaller than the capacities they hold");
+  if ((q_token_stride * esz) % 16 || (k_token_stride * esz) % 16 || (v_token_stride * esz) % 16 ||
+      (kv_head_stride * esz) % 16 || (kv_batch_stride * esz) % 16)
+    return fail(MGD_ERR_INVALID_ARG, "strides must be multiples of 16 bytes");
+  if (pos_offset && pos_offset_stride != 0 && pos_offset_stride != 1)
+    return fail(MGD_ERR_INVALID_ARG, "pos_offset_stride must be 0 or 1 (got %d)", pos_offset_stride);
+  if (B == 0) return ok();
+  if (!q || !k_new || !v_new || !turns || !kv_len || !q_out || !k || !v || !ws)
+    return fail(MGD_ERR_INVALID_ARG, "null pointer argument");
+  if (!aligned16(q) || !aligned16(k_new) || !aligned16(v_new) || !aligned16(turns) || !aligned16(q_out) ||
+      !aligned16(k) || !aligned16(v) || !aligned16(ws))
+    return fail(MGD_ERR_INVALID_ARG, "q, k_new, v_new, turns, q_out, k, v and ws must be 16-byte aligned");
+  if (q == q_out && q_token_stride != static_cast<int64_t>(Hq) * D)
+    return fail(MGD_ERR_INVALID_ARG, "q_out may be q only when q's tokens are packed");
+  if (ws_bytes < kAlign) return fail(MGD_ERR_WORKSPACE, "workspace %zu < %zu bytes", ws_bytes, kAlign);
+  RopeArgs a;
+  a.q = q;
+  a.k_new = k_new;
+  a.v_new = v_new;
+  a.q_stride = q_token_stride;
+  a.k_stride = k_token_stride;
+  a.v_stride = v_token_stride;
+  a.turns = turns;
+  a.magnitude = magnitude;
+  a.rotary_dim = rotary_dim;
+  a.interleaved = interleaved != 0;
+  a.B = B;
+  a.T = T;
+  a.Hq = Hq;
+  a.Hkv = Hkv;
+  a.D = D;
+  a.kv_cap = kv_cap;
+  a.kv_len = kv_len;
+  a.new_len = new_len;
+  a.pos_offset = pos_offset;
+  a.pos_stride = pos_offset_stride;
+  a.q_out = q_out;
+  a.k = k;
+  a.v = v;
+  a.kv_batch_stride = kv_batch_stride;
+  a.kv_head_stride = kv_head_stride;
+  a.in_f32 = dtype == MGD_F32;
+  a.ws = ws;
+  a.stream = static_cast<cudaStream_t>(stream);
+  cudaError_t e = launch_rope_append(a);
+  return e == cudaSuccess ? ok() : cuda_fail(e, "rope append launch");
+}
+
+size_t mgd_logprobs_workspace_size(int R, int V, int K) {
+  (void)R;
+  (void)V;
+  (void)K;
+  return kAlign;
+}
+
+mgd_status mgd_token_logprobs(const void *logits, int64_t row_stride, mgd_dtype dtype, const int32_t *tokens, int R,
+                              int V, int K, float *logprob, float *entropy, int32_t *rank, int32_t *top_ids,
+                              float *top_logprobs, void *ws, size_t ws_bytes, void *stream) {
+  const NvtxRange nvtx_range("mgd_token_logprobs");
+  if (R < 0) return fail(MGD_ERR_INVALID_ARG, "R must be >= 0 (got %d)", R);
+  if (V < 1) return fail(MGD_ERR_INVALID_ARG, "V must be >= 1 (got %d)", V);
+  if (K < 0 || K > 32) return fail(MGD_ERR_UNSUPPORTED, "K must be in [0, 32] (got %d)", K);
+  if (dtype != MGD_BF16 && dtype != MGD_F32) return fail(MGD_ERR_INVALID_ARG, "bad dtype %d", dtype);
+  if (row_stride < V) return fail(MGD_ERR_INVALID_ARG, "row_stride %lld < V %d", static_cast<long long>(row_stride), V);
+  if (R == 0) return ok();
+  if (!logits || !tokens || !logprob || !entropy || !rank || !ws || (K > 0 && (!top_ids || !top_logprobs)))
+    return fail(MGD_ERR_INVALID_ARG, "null pointer argument");
+  if (reinterpret_cast<uintptr_t>(logits) % (dtype == MGD_F32 ? 4 : 2) != 0)
+    return fail(MGD_ERR_INVALID_ARG, "logits must be aligned to their type");
+  if (!aligned16(ws)) return fail(MGD_ERR_INVALID_ARG, "ws must be 16-byte aligned");
+  if (ws_bytes < mgd_logprobs_workspace_size(R, V, K))
+    return fail(MGD_ERR_WORKSPACE, "workspace %zu < %zu bytes", ws_bytes, mgd_logprobs_workspace_size(R, V, K));
+  LogprobArgs a;
+  a.logits = logits;
+  a.row_stride = row_stride;
+  a.tokens = tokens;
+  a.R = R;
+  a.V = V;
+  a.K = K;
+  a.logprob = logprob;
+  a.entropy = entropy;
+  a.rank = rank;
+  a.top_ids = top_ids;
+  a.top_logprobs = top_logprobs;
+  a.in_f32 = dtype == MGD_F32;
+  a.ws = ws;
+  a.stream = static_cast<cudaStream_t>(stream);
+  cudaError_t e = launch_logprobs(a);
+  return e == cudaSuccess ? ok() : cuda_fail(e, "token logprobs launch");
 }
 
 }  // extern "C"

@@ -102,6 +102,46 @@ cudaError_t launch_attention_simt(const AttnPlan &p, const AttnArgs &a);
 int encode_kv_tensor_map(CUtensorMap *map, const void *base, int B, int Hkv, int kv_cap, int D,
                          int64_t batch_stride, int64_t head_stride, unsigned box_rows = 64);
 
+// ------------------------------------------------------------------ shared prefix
+// Rows and steps of the attention over a prefix that every sequence of the batch
+// shares (prefix.cuh).
+struct PrefixGeom {
+  int B, T, Hq, Hkv, D, G;
+  int R;          // B * T * G query rows of a KV head, ordered (b, t, g)
+  int tile_rows;  // rows of a pair
+  int RT;         // pairs per KV head
+  int key_tile;   // keys of a step
+  int last_half;  // the last pair of a head takes two key tiles a step
+  int slot_rows;  // rows kept per partial result, min(tile_rows, R)
+  int prefix_cap;
+};
+struct PrefixPlan {
+  PrefixGeom g;
+  AttnPlan own;     // attention over each sequence's own cache
+  int own_cap, grid;  // grid: CTAs of the prefix kernel
+  size_t off_own_o, off_own_l;    // float [B][T][Hq][D], [B][T][Hq]
+  size_t off_part_o, off_part_l;  // float [slots][slot_rows][D], [slots][slot_rows]
+  size_t ws_bytes;
+};
+PrefixPlan plan_prefix(int B, int T, int Hq, int Hkv, int D, int prefix_cap, int kv_cap, int in_f32, int sm_count);
+
+struct PrefixArgs {
+  const void *q;
+  const void *k;  // [Hkv, prefix_cap, D]
+  const void *v;
+  const int32_t *prefix_len;  // [1]
+  int64_t head_stride;
+  float sm_scale;
+  void *out;
+  int out_bf16;
+  float *lse;
+  void *ws;
+  cudaStream_t stream;
+};
+// Partial results over the prefix, and their merge with the own-cache results.
+cudaError_t launch_prefix_simt(const PrefixPlan &p, const PrefixArgs &a, int in_f32);
+cudaError_t launch_prefix_merge(const PrefixPlan &p, const PrefixArgs &a);
+
 // ------------------------------------------------------------------ SnapKV
 // Keys per job of the one-read tcgen05 scorer (12 tiles of 128 keys): small
 // enough that the slices open at once (one per resident CTA) mostly stay in L2
@@ -183,6 +223,41 @@ struct SpecArgs {
   cudaStream_t stream;
 };
 cudaError_t launch_spec(const SpecPlan &p, const SpecArgs &a);
+
+// ------------------------------------------------------------------ rotary positions
+struct RopeArgs {
+  const void *q, *k_new, *v_new;
+  int64_t q_stride, k_stride, v_stride;  // elements from one token's heads to the next token's
+  const void *turns;                     // uint64 [rotary_dim / 2], turns per position * 2^64
+  float magnitude;
+  int rotary_dim, interleaved;
+  int B, T, Hq, Hkv, D, kv_cap;
+  const int32_t *kv_len;
+  const int32_t *new_len;     // nullable
+  const int32_t *pos_offset;  // nullable
+  int pos_stride;
+  void *q_out, *k, *v;
+  int64_t kv_batch_stride, kv_head_stride;
+  int in_f32;
+  void *ws;
+  cudaStream_t stream;
+};
+cudaError_t launch_rope_append(const RopeArgs &a);
+
+// ------------------------------------------------------------------ log probabilities
+struct LogprobArgs {
+  const void *logits;
+  int64_t row_stride;
+  const int32_t *tokens;
+  int R, V, K;
+  float *logprob, *entropy;
+  int32_t *rank, *top_ids;
+  float *top_logprobs;
+  int in_f32;
+  void *ws;
+  cudaStream_t stream;
+};
+cudaError_t launch_logprobs(const LogprobArgs &a);
 
 // ------------------------------------------------------------------ commit / rollback
 cudaError_t launch_commit(const int32_t *num_accepted, int B, int gamma, int Hkv, int D, int esz, int32_t *kv_len,

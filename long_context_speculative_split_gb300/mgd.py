@@ -21,6 +21,7 @@ MGD_DEVERR_KV_LEN, MGD_DEVERR_SNAP_LEN, MGD_DEVERR_TOKEN, MGD_DEVERR_TIMEOUT = 0
 MGD_DEVERR_COMMIT = 0x10
 MGD_DEVERR_STALE_WS = 0x20
 MGD_DEVERR_NOT_DRAWN = 0x40
+MGD_ROPE_PLAIN, MGD_ROPE_LINEAR, MGD_ROPE_NTK, MGD_ROPE_LLAMA3, MGD_ROPE_YARN = range(5)
 
 _vp, _i32, _i64, _f32, _sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_float, ctypes.c_size_t
 
@@ -55,6 +56,16 @@ SIGNATURES = {
     "mgd_commit_round": (_i32, [_vp, _i32, _i32, _i32, _i32, _i32, _vp, _vp, _vp, _i32, _i64, _i64, _vp, _vp, _i32,
                                 _i64, _i64, _vp, _vp, _sz, _vp]),
     "mgd_spec_sample_noalloc": (_i32, [_vp, _vp, _vp, _vp, _i32, _i32, _i32, _i32, _i32, _vp, _vp, _vp]),
+    "mgd_prefix_workspace_size": (_sz, [_i32] * 7),
+    "mgd_prefix_attn": (_i32, [_vp, _vp, _vp, _vp, _i32, _i64, _vp, _vp, _vp, _i32, _i32, _i32, _i32, _i32, _i32, _i64,
+                               _i64, _f32, _i32, _vp, _i32, _vp, _vp, _sz, _vp]),
+    "mgd_rope_frequencies": (_i32, [_i32, ctypes.c_double, _i32, ctypes.POINTER(ctypes.c_double),
+                                    ctypes.POINTER(ctypes.c_uint64), ctypes.POINTER(_f32)]),
+    "mgd_rope_workspace_size": (_sz, [_i32]),
+    "mgd_rope_append": (_i32, [_vp, _i64, _vp, _i64, _vp, _i64, _vp, _f32, _i32, _i32, _i32, _i32, _i32, _i32, _i32,
+                               _i32, _vp, _vp, _vp, _i32, _vp, _vp, _vp, _i32, _i64, _i64, _vp, _sz, _vp]),
+    "mgd_logprobs_workspace_size": (_sz, [_i32] * 3),
+    "mgd_token_logprobs": (_i32, [_vp, _i64, _i32, _vp, _i32, _i32, _i32, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
 }
 
 # Bytes of the library-owned scratch array used by mgd_spec_sample_noalloc.
@@ -246,3 +257,50 @@ def mgd_spec_sample_noalloc(target_logits, draft_logits, draft_tokens, u, B, gam
     _check(load().mgd_spec_sample_noalloc(_ptr(target_logits), _ptr(draft_logits), _ptr(draft_tokens), _ptr(u),
                                           B, gamma, V, mode, row, _ptr(out_tokens), _ptr(num_accepted),
                                           _stream(stream)))
+
+
+def mgd_prefix_workspace_size(B, T, Hq, Hkv, D, prefix_cap, kv_cap):
+    return load().mgd_prefix_workspace_size(B, T, Hq, Hkv, D, prefix_cap, kv_cap)
+
+
+def mgd_prefix_attn(q, k_prefix, v_prefix, prefix_len, prefix_cap, prefix_head_stride, k, v, kv_len, B, T, Hq, Hkv, D,
+                    kv_cap, kv_batch_stride, kv_head_stride, sm_scale, in_dtype, out, out_dtype, lse, ws, ws_bytes,
+                    stream=None):
+    _check(load().mgd_prefix_attn(_ptr(q), _ptr(k_prefix), _ptr(v_prefix), _ptr(prefix_len), prefix_cap,
+                                  prefix_head_stride, _ptr(k), _ptr(v), _ptr(kv_len), B, T, Hq, Hkv, D, kv_cap,
+                                  kv_batch_stride, kv_head_stride, sm_scale, in_dtype, _ptr(out), out_dtype, _ptr(lse),
+                                  _ptr(ws), ws_bytes, _stream(stream)))
+
+
+def mgd_rope_frequencies(rotary_dim, base, scaling, params=None):
+    """-> (turns: list of rotary_dim / 2 unsigned 64-bit integers, magnitude), computed on the host."""
+    turns = (ctypes.c_uint64 * max(rotary_dim // 2, 1))()
+    mag = _f32(0.0)
+    p = None if params is None else (ctypes.c_double * 4)(*params)
+    _check(load().mgd_rope_frequencies(rotary_dim, base, scaling, p, turns, ctypes.byref(mag)))
+    return list(turns), mag.value
+
+
+def mgd_rope_workspace_size(B):
+    return load().mgd_rope_workspace_size(B)
+
+
+def mgd_rope_append(q, q_token_stride, k_new, k_token_stride, v_new, v_token_stride, turns, magnitude, rotary_dim,
+                    interleaved, B, T, Hq, Hkv, D, dtype, kv_len, new_len, pos_offset, pos_offset_stride, q_out, k, v,
+                    kv_cap, kv_batch_stride, kv_head_stride, ws, ws_bytes, stream=None):
+    _check(load().mgd_rope_append(_ptr(q), q_token_stride, _ptr(k_new), k_token_stride, _ptr(v_new), v_token_stride,
+                                  _ptr(turns), magnitude, rotary_dim, interleaved, B, T, Hq, Hkv, D, dtype,
+                                  _ptr(kv_len), _ptr(new_len), _ptr(pos_offset), pos_offset_stride, _ptr(q_out),
+                                  _ptr(k), _ptr(v), kv_cap, kv_batch_stride, kv_head_stride, _ptr(ws), ws_bytes,
+                                  _stream(stream)))
+
+
+def mgd_logprobs_workspace_size(R, V, K):
+    return load().mgd_logprobs_workspace_size(R, V, K)
+
+
+def mgd_token_logprobs(logits, row_stride, dtype, tokens, R, V, K, logprob, entropy, rank, top_ids, top_logprobs, ws,
+                       ws_bytes, stream=None):
+    _check(load().mgd_token_logprobs(_ptr(logits), row_stride, dtype, _ptr(tokens), R, V, K, _ptr(logprob),
+                                     _ptr(entropy), _ptr(rank), _ptr(top_ids), _ptr(top_logprobs), _ptr(ws), ws_bytes,
+                                     _stream(stream)))

@@ -248,3 +248,154 @@ def streaming_select(k, v, kv_len, sink, K, draft_cap=None, out=None, stream=Non
     mgd.mgd_streaming_select(k, v, kv_len, B, Hkv, D, cap, sb, sh, sink, K, _dtype_code(k), out["sel_idx"],
                              out["k_draft"], out["v_draft"], cap_d, out["draft_len"], stream)
     return out
+
+
+def prefix_attn(q, k_prefix, v_prefix, prefix_len, k, v, kv_len, sm_scale=None, out_dtype=torch.float32, ws=None,
+                out=None, lse=None, stream=None):
+    """Verify (T = 1: draft) attention of a batch over a prefix that all its sequences share and each
+    sequence's own rows behind it: q [B,T,Hq,D] (or [B,Hq,D]), k/v_prefix [Hkv,prefix_cap,D], prefix_len [1]
+    int32, own k/v [B,Hkv,kv_cap,D], kv_len [B] int32 -> (out [B,T,Hq,D], lse [B,T,Hq]) (without T for a 3-d q).
+    The prefix is read once for the whole batch."""
+    if q.dim() == 3:
+        shape, q = q.shape, q[:, None]
+    else:
+        shape = q.shape
+    B, T, Hq, D = q.shape
+    Hkv, cap = k.shape[1], k.shape[2]
+    if k_prefix.dim() != 3 or k_prefix.shape[0] != Hkv or k_prefix.shape[2] != D or v_prefix.shape != k_prefix.shape:
+        raise ValueError("k_prefix and v_prefix must be [Hkv, prefix_cap, D] = [%d, *, %d]" % (Hkv, D))
+    if k_prefix.stride(2) != 1 or k_prefix.stride(1) != D or k_prefix.stride() != v_prefix.stride():
+        raise ValueError("prefix K and V must share strides with contiguous rows of D elements")
+    if k.shape[0] != B or k.shape[3] != D or v.shape != k.shape or kv_len.numel() != B or prefix_len.numel() != 1:
+        raise ValueError("k, v must be [B, Hkv, kv_cap, D], kv_len [B] and prefix_len [1]")
+    sb, sh = _kv_strides(k, v, D)
+    scale = 1.0 / math.sqrt(D) if sm_scale is None else sm_scale
+    if out is None:
+        out = torch.empty(shape, dtype=out_dtype, device=q.device)
+    if lse is None:
+        lse = torch.empty(shape[:-1], dtype=torch.float32, device=q.device)
+    if out.shape != shape or lse.shape != shape[:-1]:
+        raise ValueError("out must have q's shape and lse the same without D")
+    _check(q.device, dense=[("q", q), ("kv_len", kv_len), ("prefix_len", prefix_len), ("out", out), ("lse", lse)],
+           int32=[("kv_len", kv_len), ("prefix_len", prefix_len)], f32=[("lse", lse)],
+           same=[("q", q), ("k_prefix", k_prefix), ("v_prefix", v_prefix), ("k", k), ("v", v)])
+    pcap = k_prefix.shape[1]
+    if ws is None:
+        ws = workspace(mgd.mgd_prefix_workspace_size(B, T, Hq, Hkv, D, pcap, cap), q.device)
+    mgd.mgd_prefix_attn(q, k_prefix, v_prefix, prefix_len, pcap, k_prefix.stride(0), k, v, kv_len, B, T, Hq, Hkv, D,
+                        cap, sb, sh, scale, _dtype_code(q), out, _dtype_code(out), lse, ws, ws.numel(), stream)
+    return out, lse
+
+
+class RopeTable:
+    """Rotary frequencies on a device: `turns` [rotary_dim / 2] int64 (the bits of unsigned turns per position
+    times 2^64) and the factor on cos and sin."""
+
+    def __init__(self, turns, magnitude, rotary_dim):
+        self.turns, self.magnitude, self.rotary_dim = turns, magnitude, rotary_dim
+
+
+_ROPE_KINDS = {"linear": (mgd.MGD_ROPE_LINEAR, ("factor",)), "ntk": (mgd.MGD_ROPE_NTK, ("factor",)),
+               "llama3": (mgd.MGD_ROPE_LLAMA3, ("factor", "low_freq_factor", "high_freq_factor", "original_len")),
+               "yarn": (mgd.MGD_ROPE_YARN, ("factor", "beta_fast", "beta_slow", "original_len"))}
+
+
+def rope_table(rotary_dim, base=10000.0, scaling=None, device="cuda"):
+    """RopeTable of `rotary_dim` elements.  scaling: None, or a dict with "kind" and that kind's values:
+    linear / ntk: factor; llama3: factor, low_freq_factor, high_freq_factor, original_len; yarn: factor,
+    beta_fast, beta_slow, original_len."""
+    code, params = mgd.MGD_ROPE_PLAIN, None
+    if scaling is not None:
+        if scaling.get("kind") not in _ROPE_KINDS:
+            raise ValueError("unknown scaling kind %r (one of %s)" % (scaling.get("kind"), ", ".join(_ROPE_KINDS)))
+        code, names = _ROPE_KINDS[scaling["kind"]]
+        if set(scaling) != {"kind", *names}:
+            raise ValueError("scaling %r takes %s" % (scaling["kind"], ", ".join(names)))
+        params = [float(scaling[n]) for n in names] + [0.0] * (4 - len(names))
+    turns, mag = mgd.mgd_rope_frequencies(rotary_dim, float(base), code, params)
+    return RopeTable(torch.tensor(turns, dtype=torch.int64, device=device), mag, rotary_dim)
+
+
+def _token_stride(name, x, B, T, H, D):
+    """Elements between two tokens' heads of a [B, T, H, D] tensor that may be a view of a fused projection."""
+    if x.dim() != 4 or tuple(x.shape) != (B, T, H, D):
+        raise ValueError("%s must be [%d, %d, %d, %d], got %s" % (name, B, T, H, D, tuple(x.shape)))
+    if x.stride(3) != 1 or (H > 1 and x.stride(2) != D):
+        raise ValueError("%s must hold a token's heads packed" % name)
+    step = x.stride(1) if T > 1 else x.stride(0) if B > 1 else H * D
+    if B > 1 and T > 1 and x.stride(0) != T * step:
+        raise ValueError("%s must hold its tokens at one stride" % name)
+    return step
+
+
+def rope_append(q, k_new, v_new, table, k, v, kv_len, new_len=None, pos_offset=None, interleaved=False, q_out=None,
+                ws=None, stream=None):
+    """Turn the new rows q [B,T,Hq,D] and k_new [B,T,Hkv,D] by their positions (RopeTable `table`), append k_new
+    and v_new to the caches k, v [B,Hkv,kv_cap,D] (in place) at rows kv_len - new_len ..  kv_len - 1, and return
+    the turned q (q_out; contiguous).  kv_len [B] int32 counts the new rows; new_len [B] int32 (default T each);
+    pos_offset [1] or [B] int32 is added to the row index to give the position."""
+    B, T, Hq, D = q.shape
+    Hkv, cap = k.shape[1], k.shape[2]
+    if k.shape[0] != B or k.shape[3] != D or v.shape != k.shape or kv_len.numel() != B:
+        raise ValueError("k, v must be [B, Hkv, kv_cap, D] and kv_len [B]")
+    sq, sk, sv = (_token_stride(n, x, B, T, h, D) for n, x, h in
+                  (("q", q, Hq), ("k_new", k_new, Hkv), ("v_new", v_new, Hkv)))
+    sb, sh = _kv_strides(k, v, D)
+    if new_len is not None and new_len.numel() != B:
+        raise ValueError("new_len must be [B]")
+    if pos_offset is not None and pos_offset.numel() not in (1, B):
+        raise ValueError("pos_offset must be [1] or [B]")
+    if q_out is None:
+        q_out = torch.zeros((B, T, Hq, D), dtype=q.dtype, device=q.device)
+    if q_out.shape != q.shape:
+        raise ValueError("q_out must have q's shape")
+    if table.turns.dtype != torch.int64 or table.turns.numel() != table.rotary_dim // 2:
+        raise TypeError("table must come from rope_table")
+    _check(q.device, dense=[("kv_len", kv_len), ("new_len", new_len), ("pos_offset", pos_offset), ("q_out", q_out),
+                            ("table", table.turns)],
+           int32=[("kv_len", kv_len), ("new_len", new_len), ("pos_offset", pos_offset)],
+           same=[("q", q), ("k_new", k_new), ("v_new", v_new), ("k", k), ("v", v), ("q_out", q_out)])
+    if ws is None:
+        ws = workspace(mgd.mgd_rope_workspace_size(B), q.device)
+    stride = 0 if pos_offset is None or pos_offset.numel() == 1 else 1
+    mgd.mgd_rope_append(q, sq, k_new, sk, v_new, sv, table.turns, table.magnitude, table.rotary_dim, int(interleaved),
+                        B, T, Hq, Hkv, D, _dtype_code(q), kv_len, new_len, pos_offset, stride, q_out, k, v, cap, sb,
+                        sh, ws, ws.numel(), stream)
+    return q_out
+
+
+def token_logprobs(logits, tokens, top=0, ws=None, out=None, stream=None):
+    """Log probabilities of `tokens` [...] int32 (-1: no token) under softmax(logits [..., V], float32 or
+    bfloat16; rows at one stride).  Returns dict(logprob [...], entropy [...] float32, rank [...] int32,
+    top_ids [..., top] int32, top_logprobs [..., top] float32)."""
+    V = logits.shape[-1]
+    if tokens.shape != logits.shape[:-1]:
+        raise ValueError("tokens must have the shape of logits without its last dimension")
+    R = tokens.numel()
+    if V > 1 and logits.stride(-1) != 1:
+        raise ValueError("logits must hold a row's entries packed")
+    dims = [(n, s) for n, s in zip(logits.shape[:-1], logits.stride()[:-1]) if n > 1]
+    step = dims[-1][1] if dims else V
+    rows = 1
+    for n, s in reversed(dims):
+        if s != step * rows:
+            raise ValueError("logits must hold its rows at one stride")
+        rows *= n
+    dev, lead = logits.device, tuple(tokens.shape)
+    if out is None:
+        out = dict(logprob=torch.empty(lead, dtype=torch.float32, device=dev),
+                   entropy=torch.empty(lead, dtype=torch.float32, device=dev),
+                   rank=torch.empty(lead, dtype=torch.int32, device=dev),
+                   top_ids=torch.empty(lead + (top,), dtype=torch.int32, device=dev),
+                   top_logprobs=torch.empty(lead + (top,), dtype=torch.float32, device=dev))
+    for name in ("logprob", "entropy", "rank", "top_ids", "top_logprobs"):
+        if tuple(out[name].shape) != (lead + (top,) if name.startswith("top") else lead):
+            raise ValueError("out[%r] has the wrong shape" % name)
+    ints = [("tokens", tokens), ("rank", out["rank"]), ("top_ids", out["top_ids"])]
+    floats = [(n, out[n]) for n in ("logprob", "entropy", "top_logprobs")]
+    _check(dev, dense=ints + floats, int32=ints, f32=floats)
+    if ws is None:
+        ws = workspace(mgd.mgd_logprobs_workspace_size(R, V, top), dev)
+    mgd.mgd_token_logprobs(logits, step, _dtype_code(logits), tokens, R, V, top, out["logprob"], out["entropy"],
+                           out["rank"], out["top_ids"], out["top_logprobs"], ws, ws.numel(), stream)
+    return out

@@ -1,0 +1,188 @@
+"""GPU parity of token_logprobs against its float64 form.
+
+Whole numbers (ranks, alternatives) are equal.  The sum of exponentials is a float32 sum of positive
+terms in chains of at most 256 additions: its relative error, and so the absolute error of its
+logarithm, is at most 256 * 2^-24 = 1.5e-5 plus a few units of the exponentials (2 * 2^-24 each) and of
+the differences x - m (|x - m| * 2^-24 each): 2e-5 + 2^-22 |value|.  The entropy's second sum has the
+same relative error times its own size.
+"""
+import math
+
+import pytest
+import torch
+
+from _parity import Guarded, check_guards, gpu_or_skip
+from _plain64 import token_logprobs as plain
+from long_context_speculative_split_gb300 import mgd, ops
+
+pytestmark = pytest.mark.gpu
+
+
+def _near(got, ref, tol):
+    if math.isnan(ref):
+        return math.isnan(got)
+    if math.isinf(ref):
+        return got == ref
+    return abs(got - ref) <= tol
+
+
+def _check(logits, tokens, K, out):
+    """Every row of the outputs against the plain form."""
+    V = logits.shape[-1]
+    x, tok = logits.reshape(-1, V), tokens.reshape(-1).tolist()
+    lp, ent, rank = (out[n].reshape(-1).tolist() for n in ("logprob", "entropy", "rank"))
+    ids, lps = (out[n].reshape(len(tok), K).tolist() for n in ("top_ids", "top_logprobs"))
+    for r in range(len(tok)):
+        if tok[r] < 0 or tok[r] >= V:
+            assert (lp[r], ent[r], rank[r]) == (0.0, 0.0, -1) and ids[r] == [-1] * K and lps[r] == [-math.inf] * K
+            continue
+        e = plain(x[r], tok[r], K)
+        assert _near(lp[r], e[0], 2e-5 + 2.0 ** -22 * abs(e[0])), (r, lp[r], e[0])
+        assert _near(ent[r], e[1], 4e-5 * (1 + abs(e[1]))), (r, ent[r], e[1])
+        assert rank[r] == e[2], (r, rank[r], e[2])
+        assert ids[r] == e[3], (r, ids[r], e[3])
+        assert all(_near(a, b, 2e-5 + 2.0 ** -22 * abs(b)) for a, b in zip(lps[r], e[4]))
+
+
+def _run(logits, tokens, K):
+    dev = logits.device
+    lead = tuple(tokens.shape)
+    g = dict(logprob=Guarded(lead, torch.float32, dev), entropy=Guarded(lead, torch.float32, dev),
+             rank=Guarded(lead, torch.int32, dev), top_ids=Guarded(lead + (K,), torch.int32, dev),
+             top_logprobs=Guarded(lead + (K,), torch.float32, dev))
+    need = mgd.mgd_logprobs_workspace_size(tokens.numel(), logits.shape[-1], K)
+    ws = Guarded((need // 4,), torch.int32, dev, init=torch.zeros(()))
+    out = ops.token_logprobs(logits, tokens, top=K, ws=ws.t.view(torch.uint8), out={n: x.t for n, x in g.items()})
+    torch.cuda.synchronize()
+    check_guards(ws=ws, **g)
+    return out, mgd.mgd_workspace_errors(ws.t)
+
+
+def _tokens(dev, R, V, seed):
+    g = torch.Generator(device=dev).manual_seed(seed)
+    return torch.randint(0, V, (R,), generator=g, device=dev).to(torch.int32)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("R,V,K", [(1, 1, 1), (2, 2, 5), (3, 31, 32), (5, 33, 8), (4, 512, 20), (3, 1000, 1), (2, 4099, 32),
+                                   (3, 16384, 7), (2, 16385, 0), (7, 50257, 3), (3, 128256, 20), (1, 128256, 32),
+                                   (2, 262145, 8), (700, 1003, 4), (1, 1000003, 5)])
+def test_rows_match_float64(R, V, K, dtype):
+    """bfloat16 rows hold many equal values: the order among them is by index."""
+    dev = gpu_or_skip()
+    g = torch.Generator(device=dev).manual_seed(V + R)
+    x = (3 * torch.randn((R, V), generator=g, device=dev)).to(dtype)
+    tok = _tokens(dev, R, V, V)
+    tok[0] = int(x[0].float().argmax())
+    out, err = _run(x, tok, K)
+    assert err == 0
+    _check(x, tok, K, out)
+
+
+def _patterns(V, dev):
+    j = torch.arange(V, device=dev, dtype=torch.float32)
+    yield "constant", torch.zeros(V, device=dev)
+    yield "lowest", torch.full((V,), torch.finfo(torch.float32).min, device=dev)
+    yield "rising", j / V
+    yield "falling", -j
+    yield "signed_zeros", torch.where(j % 2 == 0, torch.zeros_like(j), -torch.zeros_like(j))
+    yield "peak_block_first", torch.where(j < 300, 50 + j / 100, -j / V)
+    yield "peak_block_last", torch.where(j >= V - 300, 50 - j / V, j / V)
+    yield "every_512th", torch.where(j % 512 == 7, 10 + j / V, -5 + 0 * j)
+    one = torch.full((V,), -math.inf, device=dev)
+    one[V // 2] = 3.0
+    yield "one_finite", one
+    few = one.clone()
+    few[::max(V // 5, 1)] = 1.0
+    yield "few_finite", few
+    big = torch.zeros(V, device=dev)
+    big[V - 1] = 3e38
+    yield "huge", big
+    masked = torch.randn(V, device=dev)
+    masked[torch.arange(V, device=dev) % 3 != 0] = torch.finfo(torch.float32).min
+    yield "masked_with_lowest", masked
+
+
+@pytest.mark.parametrize("V", [40, 2500, 40000])
+@pytest.mark.parametrize("K", [1, 32])
+def test_adverse_orders(V, K):
+    """Ties everywhere, sorted rows, and the highest entries side by side or one stride apart."""
+    dev = gpu_or_skip()
+    names, rows = zip(*_patterns(V, dev))
+    x = torch.stack(rows)
+    for t in (0, V // 2, V - 1):
+        tok = torch.full((len(rows),), t, dtype=torch.int32, device=dev)
+        out, err = _run(x, tok, K)
+        assert err == 0
+        _check(x, tok, K, out)
+
+
+def test_rows_without_a_distribution():
+    dev = gpu_or_skip()
+    V = 3000
+    x = torch.randn((6, V), device=dev)
+    x[0, 17] = math.nan
+    x[1, V - 1] = math.inf
+    x[2] = -math.inf
+    x[3, 5] = -math.inf  # one forbidden entry: fine
+    x[5] = math.nan
+    tok = torch.tensor([17, 0, 3, 5, 9, 1], dtype=torch.int32, device=dev)
+    out, err = _run(x, tok, 4)
+    assert err == 0
+    _check(x, tok, 4, out)
+    assert out["logprob"][3] == -math.inf and torch.isnan(out["logprob"][[0, 1, 2, 5]]).all()
+
+
+def test_padding_and_bad_tokens():
+    dev = gpu_or_skip()
+    V, K = 5000, 6
+    x = torch.randn((4, 5, V), device=dev)
+    tok = _tokens(dev, 20, V, 1).view(4, 5)
+    tok[0, 2:] = -1
+    tok[3] = -1
+    x[3] = math.nan  # skipped rows are not looked at
+    out, err = _run(x, tok, K)
+    assert err == 0
+    _check(x, tok, K, out)
+    tok[1, 1], tok[2, 4] = V, -2
+    out, err = _run(x, tok, K)
+    assert err == mgd.MGD_DEVERR_TOKEN
+    _check(x, tok, K, out)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+def test_strided_and_unaligned_rows(dtype):
+    """Rows of a wider buffer (a padded vocabulary), starting at every offset within 16 bytes."""
+    dev = gpu_or_skip()
+    V, wide = 20011, 20077
+    for first in range(8):
+        buf = torch.full((3, wide), 100.0, dtype=dtype, device=dev)  # a read past V would show
+        buf[:, first:first + V] = torch.randn((3, V), device=dev).to(dtype)
+        x = buf[:, first:first + V]
+        tok = _tokens(dev, 3, V, first)
+        out, err = _run(x, tok, 5)
+        assert err == 0
+        _check(x, tok, 5, out)
+
+
+def test_scores_a_round_and_replays():
+    """The committed tokens of a round, -1 after each sequence's last, in a captured call."""
+    dev = gpu_or_skip()
+    B, gamma, V = 3, 4, 32000
+    g = torch.Generator(device=dev).manual_seed(0)
+    t = 2 * torch.randn((B, gamma + 1, V), generator=g, device=dev)
+    d = t[:, :gamma] + 0.5 * torch.randn((B, gamma, V), generator=g, device=dev)
+    u = torch.rand((B, gamma + 1, 3), generator=g, device=dev)
+    d = d.contiguous()
+    tok, n = ops.rejection_sample(t, d, ops.draft_draw(d, u), u)
+    ws = ops.workspace(mgd.mgd_logprobs_workspace_size(B * (gamma + 1), V, 3), dev)
+    out = ops.token_logprobs(t, tok, top=3, ws=ws)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        ops.token_logprobs(t, tok, top=3, ws=ws, out=out)
+    for turn in range(3):
+        t.copy_(t.roll(turn, 2))
+        graph.replay()
+        assert mgd.mgd_workspace_errors(ws) == 0
+        _check(t, tok, 3, out)

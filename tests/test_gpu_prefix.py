@@ -1,0 +1,275 @@
+"""GPU parity of shared-prefix attention against its float64 form.
+
+Tolerances: with bfloat16 inputs those of the attention calls (max-abs 2e-2, rel-L2 1e-3 on float32
+outputs); a bfloat16 output adds at most half a step, 2^-8, to the relative error.  With float32
+inputs the scores (up to about 40 in size, heavy-hitter keys) carry the rounding of a D-term float32
+sum, about sqrt(D) * 2^-24 * 40 = 3e-5 at D = 128, which is the relative error of a weight: rel-L2 1e-4.
+"""
+import math
+
+import pytest
+import torch
+
+from _parity import Guarded, assert_attention_close, assert_lse_close, check_guards, gpu_or_skip, poison_
+from _plain64 import prefix_attention
+from long_context_speculative_split_gb300 import mgd, ops
+
+pytestmark = pytest.mark.gpu
+
+
+def _inputs(dev, B, T, Hq, Hkv, D, plen, pcap, lens, cap, dtype, seed=0, pad=0):
+    """Random q, prefix and own caches with a few heavy-hitter keys; rows past the prefix's and the
+    sequences' lengths hold NaN.  pad: extra rows between two heads of the prefix (a strided view)."""
+    g = torch.Generator(device=dev).manual_seed(seed)
+
+    def rnd(*shape):
+        return torch.randn(shape, generator=g, device=dev)
+
+    q = rnd(B, T, Hq, D).to(dtype)
+    kp, vp = rnd(Hkv, pcap + pad, D), rnd(Hkv, pcap + pad, D)
+    k, v = rnd(B, Hkv, cap, D), rnd(B, Hkv, cap, D)
+    kp[:, torch.randperm(pcap, device=dev, generator=g)[:pcap // 100 + 1]] *= 8
+    k[:, :, torch.randperm(cap, device=dev, generator=g)[:cap // 100 + 1]] *= 8
+    kp, vp, k, v = (x.to(dtype) for x in (kp, vp, k, v))
+    poison_(kp[:, plen:])
+    poison_(vp[:, plen:])
+    for b in range(B):
+        poison_(k[b, :, lens[b]:])
+        poison_(v[b, :, lens[b]:])
+    return dict(q=q, k_prefix=kp[:, :pcap], v_prefix=vp[:, :pcap],
+                prefix_len=torch.tensor([plen], dtype=torch.int32, device=dev), k=k, v=v,
+                kv_len=torch.tensor(lens, dtype=torch.int32, device=dev))
+
+
+def _reference(a, scale=None):
+    D = a["q"].shape[-1]
+    return prefix_attention(a["q"], a["k_prefix"], a["v_prefix"], int(a["prefix_len"]), a["k"], a["v"],
+                            a["kv_len"].tolist(), 1.0 / math.sqrt(D) if scale is None else scale)
+
+
+def _check_close(out, lse, ref, ref_lse, dtype):
+    ref, ref_lse = ref.cpu().numpy(), ref_lse.cpu().numpy()
+    _, rel = assert_attention_close(out, ref)
+    assert_lse_close(lse, ref_lse)
+    if dtype == torch.float32:
+        assert rel <= 1e-4
+
+
+CASES = [
+    # B, T, Hq, Hkv, D, plen, pcap, lens, cap
+    (1, 1, 1, 1, 64, 1, 1, [1], 1),                          # one row, one key in each part
+    (2, 1, 8, 2, 128, 0, 16, [5, 16], 16),                   # an empty prefix
+    (2, 4, 32, 8, 128, 64, 64, [4, 77], 80),                 # kv_len == T, one 64-key tile
+    (2, 4, 32, 8, 128, 65, 200, [130, 9], 130),
+    (3, 5, 32, 8, 128, 127, 128, [64, 300, 5], 300),         # around one 128-key tile
+    (3, 5, 32, 8, 128, 128, 128, [64, 300, 5], 300),
+    (3, 5, 32, 8, 128, 129, 300, [64, 300, 5], 300),
+    (8, 4, 16, 4, 128, 257, 257, [20] * 8, 20),              # 128 rows a KV head: one block exactly
+    (9, 5, 9, 3, 64, 1000, 1000, [33] * 9, 40),              # 135 rows, three heads of three
+    (16, 4, 32, 8, 64, 700, 900, list(range(10, 26)), 30),   # 256 rows
+    (13, 4, 20, 4, 128, 1333, 1400, [50] * 13, 64),          # 260 rows: a last block of four
+    (30, 5, 10, 2, 128, 300, 300, [7] * 30, 7),              # 750 rows: three blocks, the last one short
+    (1, 2, 48, 1, 64, 4101, 4101, [300], 300),               # one KV head for 48 query heads
+    (2, 17, 32, 8, 128, 515, 515, [17, 400], 400),           # gamma 16
+    (64, 8, 8, 1, 64, 130, 130, [9] * 64, 16),               # 4096 rows over two tiles
+]
+IDS = ["B%d_T%d_H%d-%d_D%d_P%d" % c[:6] for c in CASES]
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("case", CASES, ids=IDS)
+def test_prefix_attention_matches_float64(case, dtype):
+    dev = gpu_or_skip()
+    B, T, Hq, Hkv, D, plen, pcap, lens, cap = case
+    a = _inputs(dev, B, T, Hq, Hkv, D, plen, pcap, lens, cap, dtype, seed=plen + B)
+    o, l = Guarded((B, T, Hq, D), torch.float32, dev), Guarded((B, T, Hq), torch.float32, dev)
+    ws = Guarded((mgd.mgd_prefix_workspace_size(B, T, Hq, Hkv, D, pcap, cap) // 4,), torch.int32, dev, init=torch.zeros(()))
+    ops.prefix_attn(**a, out=o.t, lse=l.t, ws=ws.t.view(torch.uint8))
+    assert mgd.mgd_workspace_errors(ws.t) == 0
+    check_guards(out=o, lse=l, ws=ws)
+    _check_close(o.t, l.t, *_reference(a), dtype)
+
+
+@pytest.mark.parametrize("B,T,Hq,Hkv,D,plen", [(128, 5, 32, 8, 128, 1500), (256, 1, 32, 8, 128, 5000),
+                                               (4, 1, 32, 8, 128, 32768), (1, 4, 32, 8, 128, 20001),
+                                               (100, 3, 6, 1, 64, 9001)])
+def test_larger_batches_and_prefixes(B, T, Hq, Hkv, D, plen):
+    """More row blocks than CTAs, and long prefixes cut over many CTAs."""
+    dev = gpu_or_skip()
+    lens = [T + (7 * b) % 40 for b in range(B)]
+    a = _inputs(dev, B, T, Hq, Hkv, D, plen, plen + 100, lens, 64, torch.bfloat16, seed=B)
+    out, lse = ops.prefix_attn(**a)
+    _check_close(out, lse, *_reference(a), torch.bfloat16)
+
+
+def test_bfloat16_output_and_draft_form():
+    dev = gpu_or_skip()
+    B, Hq, D = 6, 16, 128
+    a = _inputs(dev, B, 1, Hq, 4, D, 900, 900, [40] * B, 64, torch.bfloat16)
+    out, lse = ops.prefix_attn(**a, out_dtype=torch.bfloat16)
+    ref, ref_lse = _reference(a)
+    assert out.dtype == torch.bfloat16
+    err = (out.double() - ref).norm() / ref.norm()
+    assert float(err) <= 2.0 ** -8 + 1e-3
+    out3, lse3 = ops.prefix_attn(**dict(a, q=a["q"][:, 0]), out_dtype=torch.bfloat16)
+    assert out3.shape == (B, Hq, D) and lse3.shape == (B, Hq)
+    assert torch.equal(out3, out[:, 0]) and torch.equal(lse3, lse[:, 0])
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+def test_strided_prefix_and_own_caches(dtype):
+    """The prefix and the own caches as views with room between heads and sequences."""
+    dev = gpu_or_skip()
+    B, T, Hq, Hkv, D, plen, cap = 3, 4, 8, 2, 128, 333, 50
+    a = _inputs(dev, B, T, Hq, Hkv, D, plen, 340, [50, 4, 33], cap, dtype, pad=24)
+    wide = [poison_(torch.empty((B, Hkv + 1, cap + 8, D), dtype=dtype, device=dev)) for _ in range(2)]
+    for w, name in zip(wide, ("k", "v")):
+        w[:, :Hkv, :cap] = a[name]
+        a[name] = w[:, :Hkv, :cap]
+    out, lse = ops.prefix_attn(**a)
+    _check_close(out, lse, *_reference(a), dtype)
+
+
+@pytest.mark.parametrize("scale", [0.0, -0.05, 1.0], ids=["zero", "negative", "one"])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+def test_any_scale(scale, dtype):
+    dev = gpu_or_skip()
+    a = _inputs(dev, 5, 3, 8, 2, 64, 200, 260, [3, 9, 40, 41, 42], 50, dtype)
+    a["q"] = (a["q"].float() * 0.25).to(dtype)  # scores at scale 1 stay within float32's exponent range
+    out, lse = ops.prefix_attn(**a, sm_scale=scale)
+    _check_close(out, lse, *_reference(a, scale), dtype)
+
+
+@pytest.mark.parametrize("vmax", [1e-3, 6.0e4], ids=["tiny_V", "V_near_f16_max"])
+def test_v_across_the_float16_range(vmax):
+    dev = gpu_or_skip()
+    a = _inputs(dev, 8, 5, 32, 8, 128, 1000, 1000, [60] * 8, 64, torch.bfloat16)
+    for n in ("v", "v_prefix"):
+        a[n] = (a[n].float() * (vmax / 6.0)).clamp(-vmax, vmax).to(torch.bfloat16)
+    out, _ = ops.prefix_attn(**a)
+    ref, _ = _reference(a)
+    assert bool(torch.isfinite(out).all())
+    assert float((out.double() - ref).norm() / ref.norm()) <= 1e-3
+
+
+def test_growing_scores_rescale_the_running_result():
+    """Keys whose scores grow along the prefix, so that every tile raises the running maximum, and
+    fall along it, so that only the first does."""
+    dev = gpu_or_skip()
+    B, T, Hq, Hkv, D, plen = 10, 4, 16, 4, 128, 1100
+    for sign in (1.0, -1.0):
+        a = _inputs(dev, B, T, Hq, Hkv, D, plen, plen, [12] * B, 12, torch.bfloat16)
+        ramp = torch.linspace(-1.0, 1.0, plen, device=dev)[None, :, None] * sign
+        a["k_prefix"] = (a["k_prefix"].float() * 0.1 + 12.0 * ramp).to(torch.bfloat16)
+        a["q"] = (a["q"].float().abs()).to(torch.bfloat16)
+        out, lse = ops.prefix_attn(**a)
+        ref, ref_lse = _reference(a)
+        assert float((out.double() - ref).norm() / ref.norm()) <= 1e-3
+        # scores reach about 100: their float32 sums are good to 100 * sqrt(D) * 2^-24 < 1e-4
+        assert float((lse.double() - ref_lse).abs().max()) <= 1e-3
+
+
+def test_masked_keys_of_minus_infinity_scores():
+    """A prefix whose every score is -inf for some rows (keys with an infinite component against a
+    query of the other sign): those rows see their own cache only."""
+    dev = gpu_or_skip()
+    for dtype in (torch.float32, torch.bfloat16):
+        a = _inputs(dev, 4, 2, 4, 1, 64, 130, 130, [20] * 4, 20, dtype)
+        a["k_prefix"] = a["k_prefix"].clone()
+        a["k_prefix"][:, :, 0] = math.inf
+        a["q"] = a["q"].clone()
+        a["q"][..., 0] = -1.0
+        a["k"][..., 0] = 0.0
+        out, lse = ops.prefix_attn(**a)
+        none = dict(a, prefix_len=torch.zeros_like(a["prefix_len"]))
+        ref, ref_lse = _reference(none)
+        _check_close(out, lse, ref, ref_lse, dtype)
+
+
+def test_equals_verify_attention_over_the_concatenation():
+    dev = gpu_or_skip()
+    B, T, Hq, Hkv, D, plen, cap = 4, 4, 32, 8, 128, 777, 96
+    lens = [96, 4, 50, 51]
+    a = _inputs(dev, B, T, Hq, Hkv, D, plen, plen, lens, cap, torch.bfloat16)
+    k = torch.cat((a["k_prefix"][None].expand(B, -1, -1, -1), a["k"]), 2).contiguous()
+    v = torch.cat((a["v_prefix"][None].expand(B, -1, -1, -1), a["v"]), 2).contiguous()
+    out, lse = ops.prefix_attn(**a)
+    out2, lse2 = ops.verify_attn(a["q"], k, v, a["kv_len"] + plen)
+    # both within 1e-3 (rel-L2) and 1e-3 (lse) of the exact values
+    assert float((out - out2).norm() / out2.norm()) <= 2e-3
+    assert float((lse - lse2).abs().max()) <= 2e-3
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+def test_bad_lengths_are_flagged(dtype):
+    dev = gpu_or_skip()
+    B, T, Hq, Hkv, D, plen, pcap, cap = 3, 2, 8, 2, 64, 100, 128, 32
+    a = _inputs(dev, B, T, Hq, Hkv, D, plen, pcap, [10, 11, 12], cap, dtype)
+    ws = ops.workspace(mgd.mgd_prefix_workspace_size(B, T, Hq, Hkv, D, pcap, cap), dev)
+    good, good_lse = ops.prefix_attn(**a, ws=ws)
+    assert mgd.mgd_workspace_errors(ws) == 0
+    for bad in (-1, pcap + 1):
+        ops.prefix_attn(**dict(a, prefix_len=torch.full_like(a["prefix_len"], bad)), ws=ws)
+        assert mgd.mgd_workspace_errors(ws) == mgd.MGD_DEVERR_KV_LEN
+    out, lse = ops.prefix_attn(**a, ws=ws)
+    assert mgd.mgd_workspace_errors(ws) == 0, "an error outlived its call"
+    assert torch.equal(out, good) and torch.equal(lse, good_lse)
+    lens = a["kv_len"].clone()
+    lens[1] = cap + 1
+    out, lse = ops.prefix_attn(**dict(a, kv_len=lens), ws=ws)
+    assert mgd.mgd_workspace_errors(ws) == mgd.MGD_DEVERR_KV_LEN
+    assert torch.equal(out[0], good[0]) and torch.equal(out[2], good[2])
+
+
+def test_one_workspace_serves_every_shape_and_results_repeat():
+    dev = gpu_or_skip()
+    shapes = [(8, 4, 16, 4, 128, 600), (1, 1, 4, 1, 64, 3000), (40, 5, 32, 8, 128, 300), (2, 2, 8, 8, 128, 90)]
+    need = max(mgd.mgd_prefix_workspace_size(*s, 64) for s in shapes)
+    ws = ops.workspace(need, dev)
+    first = {}
+    for turn in range(2):
+        for i, (B, T, Hq, Hkv, D, P) in enumerate(shapes):
+            a = _inputs(dev, B, T, Hq, Hkv, D, P, P, [T + b % 30 for b in range(B)], 64, torch.bfloat16, seed=i)
+            out, lse = ops.prefix_attn(**a, ws=ws)
+            assert mgd.mgd_workspace_errors(ws) == 0
+            if turn == 0:
+                first[i] = (out, lse)
+                _check_close(out, lse, *_reference(a), torch.bfloat16)
+            else:
+                assert torch.equal(out, first[i][0]) and torch.equal(lse, first[i][1])
+
+
+def test_captured_call_follows_the_lengths_on_the_device():
+    """A captured call, replayed with other lengths: the work is partitioned on the device."""
+    dev = gpu_or_skip()
+    B, T, Hq, Hkv, D, pcap, cap = 12, 4, 16, 4, 128, 2000, 64
+    a = _inputs(dev, B, T, Hq, Hkv, D, pcap, pcap, [64] * B, cap, torch.bfloat16)
+    ws = ops.workspace(mgd.mgd_prefix_workspace_size(B, T, Hq, Hkv, D, pcap, cap), dev)
+    out, lse = ops.prefix_attn(**a, ws=ws)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        ops.prefix_attn(**a, ws=ws, out=out, lse=lse)
+    for plen, L in ((2000, 64), (1, 4), (0, 17), (1153, 40), (128, 64)):
+        a["prefix_len"].fill_(plen)
+        a["kv_len"].fill_(L)
+        g.replay()
+        assert mgd.mgd_workspace_errors(ws) == 0
+        _check_close(out, lse, *_reference(a), torch.bfloat16)
+
+
+def test_two_streams_with_their_own_workspaces():
+    dev = gpu_or_skip()
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    ins = [_inputs(dev, 16, 4, 32, 8, 128, 3000, 3000, [30] * 16, 32, torch.bfloat16, seed=s) for s in (1, 2)]
+    serial = [ops.prefix_attn(**a) for a in ins]
+    wss = [ops.workspace(mgd.mgd_prefix_workspace_size(16, 4, 32, 8, 128, 3000, 32), dev) for _ in ins]
+    outs = [(torch.empty_like(o), torch.empty_like(l)) for o, l in serial]
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for a, w, (o, l), s in zip(ins, wss, outs, (s1, s2)):
+            ops.prefix_attn(**a, ws=w, out=o, lse=l, stream=s)
+    torch.cuda.synchronize()
+    for (o, l), (ro, rl), w in zip(outs, serial, wss):
+        assert mgd.mgd_workspace_errors(w) == 0
+        assert torch.equal(o, ro) and torch.equal(l, rl)

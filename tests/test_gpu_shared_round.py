@@ -1,0 +1,104 @@
+"""The operators of a batch with a shared prompt, run together as a serving loop would: new rows are
+turned and appended behind the shared prefix, attended over prefix and own cache, sampled, and their
+log probabilities taken; then the round is committed."""
+import math
+
+import pytest
+import torch
+
+from _parity import assert_attention_close, gpu_or_skip
+from _plain64 import prefix_attention, rope, rope_radians
+from _plain64 import token_logprobs as plain_logprobs
+from long_context_speculative_split_gb300 import mgd, ops
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("captured", [False, True], ids=["eager", "captured"])
+def test_two_rounds_behind_a_shared_prefix(captured):
+    dev = gpu_or_skip()
+    B, gamma, Hq, Hkv, D, P, cap, V = 6, 3, 16, 4, 128, 500, 64, 4000
+    T = gamma + 1
+    g = torch.Generator(device=dev).manual_seed(11)
+
+    def rnd(*s):
+        return torch.randn(s, generator=g, device=dev)
+
+    bf, i32 = torch.bfloat16, dict(dtype=torch.int32, device=dev)
+    table = ops.rope_table(D, 500000.0, dict(kind="llama3", factor=8.0, low_freq_factor=1.0, high_freq_factor=4.0,
+                                             original_len=8192), device=dev)
+    inv, mag = rope_radians(D, 500000.0, dict(kind="llama3", factor=8.0, low_freq_factor=1.0, high_freq_factor=4.0,
+                                              original_len=8192))
+    # the shared prefix is itself a prefill through rope_append: one sequence of P rows at positions 0 .. P - 1
+    kp, vp = torch.zeros((1, Hkv, P, D), dtype=bf, device=dev), torch.zeros((1, Hkv, P, D), dtype=bf, device=dev)
+    praw = rnd(1, P, Hkv, D).to(bf)
+    ops.rope_append(rnd(1, P, Hq, D).to(bf), praw, rnd(1, P, Hkv, D).to(bf), table, kp, vp, torch.tensor([P], **i32))
+    prefix_len = torch.tensor([P], **i32)
+
+    k, v = torch.zeros((B, Hkv, cap, D), dtype=bf, device=dev), torch.zeros((B, Hkv, cap, D), dtype=bf, device=dev)
+    kd, vd = torch.zeros_like(k), torch.zeros_like(v)
+    kv_len, draft_len = torch.zeros(B, **i32), torch.zeros(B, **i32)
+    qkv, out_tok = rnd(B, T, Hq + 2 * Hkv, D).to(bf), torch.empty((B, T), **i32)
+    tl, u = 2 * rnd(B, T, V), torch.rand((B, T, 3), generator=g, device=dev)
+    dl = (tl[:, :gamma] + 0.5 * rnd(B, gamma, V)).contiguous()
+    tok, nacc = torch.empty((B, gamma), **i32), torch.empty((B,), **i32)
+    q = torch.empty((B, T, Hq, D), dtype=bf, device=dev)
+    out, lse = torch.empty((B, T, Hq, D), device=dev), torch.empty((B, T, Hq), device=dev)
+    ws = dict(rope=mgd.mgd_rope_workspace_size(B), attn=mgd.mgd_prefix_workspace_size(B, T, Hq, Hkv, D, P, cap),
+              spec=mgd.mgd_spec_workspace_size(B, gamma, V), lp=mgd.mgd_logprobs_workspace_size(B * T, V, 4),
+              commit=mgd.mgd_commit_workspace_size(B))
+    ws = {n: ops.workspace(s, dev) for n, s in ws.items()}
+    lp = dict(logprob=torch.empty((B, T), device=dev), entropy=torch.empty((B, T), device=dev),
+              rank=torch.empty((B, T), **i32), top_ids=torch.empty((B, T, 4), **i32),
+              top_logprobs=torch.empty((B, T, 4), device=dev))
+    seen = torch.empty(B, **i32)
+
+    def one_round():
+        kv_len.add_(T)
+        seen.copy_(kv_len)
+        ops.rope_append(qkv[:, :, :Hq], qkv[:, :, Hq:Hq + Hkv], qkv[:, :, Hq + Hkv:], table, k, v, kv_len,
+                        pos_offset=prefix_len, q_out=q, ws=ws["rope"])
+        ops.prefix_attn(q, kp[0], vp[0], prefix_len, k, v, kv_len, ws=ws["attn"], out=out, lse=lse)
+        ops.draft_draw(dl, u, draft_tokens=tok, ws=ws["spec"])
+        ops.rejection_sample(tl, dl, tok, u, ws=ws["spec"], out_tokens=out_tok, num_accepted=nacc,
+                             reuse_draft_stats=True)
+        ops.token_logprobs(tl, out_tok, top=4, ws=ws["lp"], out=lp)
+        ops.commit_round(nacc, gamma, kv_len, k, v, kd, vd, draft_len, ws=ws["commit"])
+
+    play = one_round
+    if captured:
+        one_round()
+        torch.cuda.synchronize()
+        kv_len.zero_()
+        draft_len.zero_()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            one_round()
+        play = graph.replay
+    for _ in range(2):
+        qkv.copy_(rnd(*qkv.shape).to(bf))
+        before = kv_len.clone()
+        play()
+        torch.cuda.synchronize()
+        assert all(mgd.mgd_workspace_errors(w) == 0 for w in ws.values())
+        for b in range(B):
+            L = int(before[b]) + T
+            pos = torch.arange(P + L - T, P + L, device=dev)
+            for got, x in ((q[b], qkv[b, :, :Hq]), (k[b, :, L - T:L].transpose(0, 1), qkv[b, :, Hq:Hq + Hkv])):
+                ref = rope(x, pos, inv, mag, False)
+                # half a step of bfloat16, and the float32 error of a value near a cancellation
+                assert bool(((got.double() - ref).abs() <= 2.0 ** -8 * ref.abs() + 1e-5).all())
+            assert torch.equal(v[b, :, L - T:L].transpose(0, 1), qkv[b, :, Hq + Hkv:])
+        ref, ref_lse = prefix_attention(q, kp[0], vp[0], P, k, v, seen.tolist(), 1.0 / math.sqrt(D))
+        assert_attention_close(out, ref.cpu().numpy())
+        assert float((lse.double() - ref_lse).abs().max()) <= 1e-3
+        n = nacc.tolist()
+        for b in range(B):
+            for t in range(T):
+                if t > n[b]:
+                    assert int(out_tok[b, t]) == -1 and float(lp["logprob"][b, t]) == 0.0
+                    continue
+                e = plain_logprobs(tl[b, t], int(out_tok[b, t]), 4)
+                assert abs(float(lp["logprob"][b, t]) - e[0]) <= 2e-5 + 2.0 ** -22 * abs(e[0])
+                assert int(lp["rank"][b, t]) == e[2] and lp["top_ids"][b, t].tolist() == e[3]
+        assert kv_len.tolist() == [int(before[b]) + 1 + n[b] for b in range(B)]

@@ -1,0 +1,193 @@
+"""Host-side refusals of shared-prefix attention, rope_append and token_logprobs (no GPU: every call
+fails before a launch), and the rotary frequencies, which are host arithmetic."""
+import math
+
+import pytest
+import torch
+
+from _plain64 import rope_radians
+from long_context_speculative_split_gb300 import build, mgd, ops
+
+FAKE = 1 << 20  # aligned, never dereferenced
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    build.build()
+
+
+def _status(fn, base, kw):
+    try:
+        fn(**dict(base, **kw))
+        return 0
+    except mgd.MgdError as e:
+        return e.status
+
+
+PREFIX = dict(q=FAKE, k_prefix=FAKE, v_prefix=FAKE, prefix_len=FAKE, prefix_cap=512, prefix_head_stride=512 * 128, k=FAKE,
+              v=FAKE, kv_len=FAKE, B=2, T=4, Hq=8, Hkv=2, D=128, kv_cap=64, kv_batch_stride=2 * 64 * 128,
+              kv_head_stride=64 * 128, sm_scale=0.1, in_dtype=0, out=FAKE, out_dtype=1, lse=None, ws=FAKE,
+              ws_bytes=1 << 40, stream=0)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(D=96), 2), (dict(T=0), 1), (dict(T=18), 1), (dict(Hq=6, Hkv=4), 1), (dict(B=-1), 1), (dict(prefix_cap=0), 1),
+    (dict(prefix_head_stride=512 * 128 - 8), 1), (dict(prefix_head_stride=512 * 128 + 4), 1), (dict(k_prefix=None), 1),
+    (dict(v_prefix=FAKE + 8), 1), (dict(prefix_len=None), 1), (dict(kv_head_stride=100), 1), (dict(in_dtype=5), 1),
+    (dict(out_dtype=5), 1), (dict(ws=None), 1), (dict(ws_bytes=4096), 3),
+    (dict(B=1 << 26, kv_batch_stride=1 << 40), 2)])
+def test_prefix_attention_refuses(kw, status):
+    assert _status(mgd.mgd_prefix_attn, PREFIX, kw) == status and mgd.mgd_last_error()
+
+
+def test_empty_batches_are_no_ops():
+    none = dict(q=None, k=None, v=None, kv_len=None, ws=None, B=0)
+    assert _status(mgd.mgd_prefix_attn, PREFIX, dict(none, k_prefix=None, v_prefix=None, prefix_len=None, out=None)) == 0
+    assert _status(mgd.mgd_rope_append, ROPE, dict(none, k_new=None, v_new=None, turns=None, q_out=None)) == 0
+    assert _status(mgd.mgd_token_logprobs, LOGP, dict(R=0, logits=None, tokens=None, logprob=None, entropy=None, rank=None,
+                                                      top_ids=None, top_logprobs=None, ws=None)) == 0
+
+
+def test_workspace_sizes():
+    a = mgd.mgd_prefix_workspace_size(128, 5, 32, 8, 128, 32768, 1024)
+    assert a == mgd.mgd_prefix_workspace_size(128, 5, 32, 8, 128, 32768, 1024) > 128 * 5 * 32 * 128 * 4
+    assert mgd.mgd_prefix_workspace_size(1, 1, 32, 8, 128, 32768, 64) < a
+    assert mgd.mgd_prefix_workspace_size(0, 5, 32, 8, 128, 64, 64) == 256
+    assert mgd.mgd_rope_workspace_size(4) >= 256 and mgd.mgd_logprobs_workspace_size(4, 1000, 5) >= 256
+
+
+ROPE = dict(q=FAKE, q_token_stride=8 * 64, k_new=FAKE, k_token_stride=2 * 64, v_new=FAKE, v_token_stride=2 * 64, turns=FAKE,
+            magnitude=1.0, rotary_dim=64, interleaved=0, B=2, T=3, Hq=8, Hkv=2, D=64, dtype=0, kv_len=FAKE, new_len=None,
+            pos_offset=None, pos_offset_stride=0, q_out=FAKE, k=FAKE, v=FAKE, kv_cap=32, kv_batch_stride=2 * 32 * 64,
+            kv_head_stride=32 * 64, ws=FAKE, ws_bytes=256, stream=0)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(B=-1), 1), (dict(T=0), 1), (dict(D=60, rotary_dim=60), 2), (dict(rotary_dim=63), 1), (dict(rotary_dim=0), 1),
+    (dict(rotary_dim=66), 1), (dict(dtype=3), 1), (dict(q_token_stride=8 * 64 - 8), 1), (dict(k_token_stride=2 * 64 + 4), 1),
+    (dict(v_token_stride=64), 1), (dict(kv_head_stride=31 * 64), 1), (dict(kv_batch_stride=32 * 64), 1),
+    (dict(turns=None), 1), (dict(kv_len=None), 1), (dict(k_new=FAKE + 2), 1), (dict(q_out=None), 1),
+    (dict(pos_offset=FAKE, pos_offset_stride=2), 1), (dict(q_token_stride=16 * 64), 1), (dict(ws_bytes=8), 3),
+    (dict(ws=None), 1), (dict(B=1 << 20, T=1 << 12), 2)])
+def test_rope_append_refuses(kw, status):
+    assert _status(mgd.mgd_rope_append, ROPE, kw) == status and mgd.mgd_last_error()
+
+
+LOGP = dict(logits=FAKE, row_stride=1000, dtype=1, tokens=FAKE, R=4, V=1000, K=3, logprob=FAKE, entropy=FAKE, rank=FAKE,
+            top_ids=FAKE, top_logprobs=FAKE, ws=FAKE, ws_bytes=1 << 30, stream=0)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(R=-1), 1), (dict(V=0), 1), (dict(K=33), 2), (dict(K=-1), 2), (dict(dtype=4), 1), (dict(row_stride=999), 1),
+    (dict(logits=None), 1), (dict(tokens=None), 1), (dict(top_ids=None), 1), (dict(top_logprobs=None), 1),
+    (dict(logits=FAKE + 2), 1), (dict(logits=FAKE + 1, dtype=0), 1), (dict(ws=None), 1), (dict(ws_bytes=8), 3)])
+def test_token_logprobs_refuses(kw, status):
+    assert _status(mgd.mgd_token_logprobs, LOGP, kw) == status and mgd.mgd_last_error()
+
+
+@pytest.mark.parametrize("base", [10000.0, 500000.0])
+@pytest.mark.parametrize("rot", [2, 4, 64, 128])
+@pytest.mark.parametrize("scaling", [None, dict(kind="linear", factor=4.0), dict(kind="ntk", factor=3.5),
+                                     dict(kind="llama3", factor=8.0, low_freq_factor=1.0, high_freq_factor=4.0,
+                                          original_len=8192),
+                                     dict(kind="yarn", factor=16.0, beta_fast=32.0, beta_slow=1.0, original_len=4096)],
+                         ids=lambda s: "plain" if s is None else s["kind"])
+def test_frequencies_match_the_formulas(base, rot, scaling):
+    if rot == 2 and scaling is not None and scaling["kind"] == "ntk":
+        with pytest.raises(mgd.MgdError):
+            ops.rope_table(rot, base, scaling, device="cpu")
+        return
+    table = ops.rope_table(rot, base, scaling, device="cpu")
+    inv, mag = rope_radians(rot, base, scaling)
+    assert table.turns.numel() == rot // 2 and table.magnitude == pytest.approx(mag, rel=2.0 ** -24)
+    for got, x in zip(table.turns.tolist(), inv):
+        # pow, log and the products in float64: a few units of 2^-53
+        assert got / 2.0 ** 64 == pytest.approx(x / (2 * math.pi), rel=1e-13)
+
+
+@pytest.mark.parametrize("kw", [
+    dict(rotary_dim=7), dict(rotary_dim=0), dict(base=1.0), dict(base=math.inf), dict(base=math.nan),
+    dict(scaling=dict(kind="linear", factor=0.5)), dict(scaling=dict(kind="linear", factor=math.nan)),
+    dict(scaling=dict(kind="llama3", factor=8.0, low_freq_factor=4.0, high_freq_factor=4.0, original_len=8192)),
+    dict(scaling=dict(kind="yarn", factor=8.0, beta_fast=1.0, beta_slow=32.0, original_len=4096)),
+    dict(scaling=dict(kind="yarn", factor=8.0, beta_fast=32.0, beta_slow=1.0, original_len=0))])
+def test_frequencies_refuse(kw):
+    with pytest.raises(mgd.MgdError):
+        ops.rope_table(**dict(dict(rotary_dim=64, device="cpu"), **kw))
+
+
+def test_scaling_names_are_checked():
+    with pytest.raises(ValueError, match="unknown scaling kind"):
+        ops.rope_table(64, scaling=dict(kind="other", factor=2.0), device="cpu")
+    with pytest.raises(ValueError, match="takes factor"):
+        ops.rope_table(64, scaling=dict(kind="linear"), device="cpu")
+
+
+def _prefix_args(dtype=torch.bfloat16):
+    B, T, Hq, Hkv, D = 2, 3, 8, 2, 64
+    return dict(q=torch.zeros((B, T, Hq, D), dtype=dtype), k_prefix=torch.zeros((Hkv, 16, D), dtype=dtype),
+                v_prefix=torch.zeros((Hkv, 16, D), dtype=dtype), prefix_len=torch.ones(1, dtype=torch.int32),
+                k=torch.zeros((B, Hkv, 8, D), dtype=dtype), v=torch.zeros((B, Hkv, 8, D), dtype=dtype),
+                kv_len=torch.full((B,), 8, dtype=torch.int32))
+
+
+def test_prefix_wrapper_refuses_what_the_pointers_would_hide():
+    a = _prefix_args()
+    with pytest.raises(TypeError, match="prefix_len must be int32"):
+        ops.prefix_attn(**dict(a, prefix_len=a["prefix_len"].long()))
+    with pytest.raises(ValueError, match="prefix_len"):
+        ops.prefix_attn(**dict(a, prefix_len=torch.ones(2, dtype=torch.int32)))
+    with pytest.raises(ValueError, match="k_prefix"):
+        ops.prefix_attn(**dict(a, k_prefix=a["k_prefix"][:1], v_prefix=a["v_prefix"][:1]))
+    with pytest.raises(ValueError, match="share strides"):
+        ops.prefix_attn(**dict(a, v_prefix=torch.zeros((2, 20, 64), dtype=torch.bfloat16)[:, :16]))
+    with pytest.raises(TypeError, match="v_prefix has dtype"):
+        ops.prefix_attn(**dict(a, v_prefix=a["v_prefix"].float()))
+    with pytest.raises(ValueError, match="q must be contiguous"):
+        ops.prefix_attn(**dict(a, q=torch.zeros((3, 2, 8, 64), dtype=torch.bfloat16).transpose(0, 1)))
+    with pytest.raises(ValueError, match="kv_len is on meta"):
+        ops.prefix_attn(**dict(a, kv_len=torch.empty((2,), dtype=torch.int32, device="meta")))
+    with pytest.raises(ValueError, match="out must have"):
+        ops.prefix_attn(**a, out=torch.zeros((2, 3, 8, 32)))
+
+
+def test_rope_wrapper_refuses_what_the_pointers_would_hide():
+    B, T, Hq, Hkv, D = 2, 3, 4, 2, 64
+    z = lambda *s: torch.zeros(s, dtype=torch.bfloat16)  # noqa: E731
+    table = ops.rope_table(64, device="cpu")
+    a = dict(q=z(B, T, Hq, D), k_new=z(B, T, Hkv, D), v_new=z(B, T, Hkv, D), table=table, k=z(B, Hkv, 8, D),
+             v=z(B, Hkv, 8, D), kv_len=torch.full((B,), 8, dtype=torch.int32))
+    with pytest.raises(ValueError, match="heads packed"):
+        ops.rope_append(**dict(a, q=z(B, Hq, T, D).transpose(1, 2)))
+    with pytest.raises(ValueError, match="one stride"):
+        ops.rope_append(**dict(a, q=z(B, T + 1, Hq, D)[:, :T]))
+    with pytest.raises(ValueError, match="k_new must be"):
+        ops.rope_append(**dict(a, k_new=z(B, T, Hkv + 1, D)))
+    with pytest.raises(TypeError, match="new_len must be int32"):
+        ops.rope_append(**a, new_len=torch.ones(B, dtype=torch.int64))
+    with pytest.raises(ValueError, match="pos_offset"):
+        ops.rope_append(**a, pos_offset=torch.ones(3, dtype=torch.int32))
+    with pytest.raises(TypeError, match="v has dtype"):
+        ops.rope_append(**dict(a, v=a["v"].float()))
+    with pytest.raises(ValueError, match="q_out must be contiguous"):
+        ops.rope_append(**a, q_out=z(B, Hq, T, D).transpose(1, 2))
+    with pytest.raises(TypeError, match="table"):
+        ops.rope_append(**dict(a, table=ops.RopeTable(table.turns[:3], 1.0, 64)))
+
+
+def test_logprobs_wrapper_refuses_what_the_pointers_would_hide():
+    x, tok = torch.zeros((2, 3, 100)), torch.zeros((2, 3), dtype=torch.int32)
+    with pytest.raises(ValueError, match="shape of logits"):
+        ops.token_logprobs(x, tok[0])
+    with pytest.raises(TypeError, match="tokens must be int32"):
+        ops.token_logprobs(x, tok.long())
+    with pytest.raises(ValueError, match="entries packed"):
+        ops.token_logprobs(torch.zeros((100, 2, 3)).permute(1, 2, 0), tok)
+    with pytest.raises(ValueError, match="one stride"):
+        ops.token_logprobs(torch.zeros((2, 4, 100))[:, :3], tok)
+    with pytest.raises(TypeError, match="unsupported dtype"):
+        ops.token_logprobs(x.half(), tok, ws=torch.zeros(256, dtype=torch.uint8))
+    out = dict(logprob=torch.zeros(2, 3), entropy=torch.zeros(2, 3), rank=tok.clone(),
+               top_ids=torch.zeros((2, 3, 4), dtype=torch.int32), top_logprobs=torch.zeros(2, 3, 4))
+    with pytest.raises(ValueError, match="top_ids"):
+        ops.token_logprobs(x, tok, top=5, out=out)

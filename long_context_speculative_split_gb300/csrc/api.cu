@@ -536,10 +536,18 @@ mgd_status mgd_prefix_attn(const void *q, const void *k_prefix, const void *v_pr
   };
   // The float32 attention clears the header ahead of its launch, so the prefix kernel raises its
   // bits after it; the bf16 one closes the call's error word, so there the prefix goes first.
-  if (in_f32 && (s = own()) != MGD_OK) return s;
-  cudaError_t e = launch_prefix_simt(plan, a, in_f32);
+  cudaError_t e;
+  if (in_f32) {
+    if ((s = own()) != MGD_OK) return s;
+    e = launch_prefix_simt(plan, a);
+  } else {
+    CUtensorMap km;
+    if (encode_kv_tensor_map(&km, k_prefix, 1, Hkv, prefix_cap, D, prefix_head_stride * Hkv, prefix_head_stride, 128) != 0)
+      return fail(MGD_ERR_CUDA, "cuTensorMapEncodeTiled failed");
+    e = launch_prefix_tc05(plan, a, km);
+    if (e == cudaSuccess && (s = own()) != MGD_OK) return s;
+  }
   if (e != cudaSuccess) return cuda_fail(e, "prefix attention launch");
-  if (!in_f32 && (s = own()) != MGD_OK) return s;
   e = launch_prefix_merge(plan, a);
   return e == cudaSuccess ? ok() : cuda_fail(e, "prefix merge launch");
 }

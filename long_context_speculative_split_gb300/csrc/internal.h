@@ -139,7 +139,8 @@ struct PrefixArgs {
   cudaStream_t stream;
 };
 // Partial results over the prefix, and their merge with the own-cache results.
-cudaError_t launch_prefix_simt(const PrefixPlan &p, const PrefixArgs &a, int in_f32);
+cudaError_t launch_prefix_tc05(const PrefixPlan &p, const PrefixArgs &a, const CUtensorMap &kmap);  // bf16
+cudaError_t launch_prefix_simt(const PrefixPlan &p, const PrefixArgs &a);                           // float32
 cudaError_t launch_prefix_merge(const PrefixPlan &p, const PrefixArgs &a);
 
 // ------------------------------------------------------------------ SnapKV

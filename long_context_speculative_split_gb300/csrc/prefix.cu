@@ -1,6 +1,6 @@
 // Attention over a prefix that every sequence of a batch shares, computed once
-// for all of them: the plan, the CUDA-core kernel, and the merge of the prefix
-// part with the part over each sequence's own cache.
+// for all of them: the plan, the CUDA-core kernel for float32 inputs, and the merge of
+// the prefix part with the part over each sequence's own cache.
 //
 // With s_j = scale <q, k_j>, the softmax over prefix and own keys splits exactly:
 //   (O_P, l_P), (O_b, l_b) = the two parts' outputs and log-sum-exps
@@ -36,20 +36,11 @@ struct SimtLayout {
   static constexpr int bytes = (off_p + kSRows * kPStride) * 4;
 };
 
-template <typename Tin>
-__device__ __forceinline__ float4 load4(const Tin *p);
-template <>
-__device__ __forceinline__ float4 load4<float>(const float *p) { return *reinterpret_cast<const float4 *>(p); }
-template <>
-__device__ __forceinline__ float4 load4<__nv_bfloat16>(const __nv_bfloat16 *p) {
-  const uint2 x = *reinterpret_cast<const uint2 *>(p);
-  return make_float4(__uint_as_float(x.x << 16), __uint_as_float(x.x & 0xFFFF0000u), __uint_as_float(x.y << 16),
-                     __uint_as_float(x.y & 0xFFFF0000u));
-}
+__device__ __forceinline__ float4 load4(const float *p) { return *reinterpret_cast<const float4 *>(p); }
 
-template <typename Tin, int D>
+template <int D>
 __global__ void __launch_bounds__(kSThreads)
-    prefix_simt_kernel(const Tin *__restrict__ q, const Tin *__restrict__ k, const Tin *__restrict__ v,
+    prefix_simt_kernel(const float *__restrict__ q, const float *__restrict__ k, const float *__restrict__ v,
                        const int32_t *__restrict__ prefix_len, int64_t head_stride, float sl2, PrefixGeom g,
                        float *__restrict__ part_o, float *__restrict__ part_l, WsHeader *hdr) {
   pdl_launch_dependents();
@@ -245,24 +236,23 @@ __global__ void __launch_bounds__(kMergeWarps * 32)
   if (lse_out && lane == 0) lse_out[row] = m + logf(wsum);
 }
 
-template <typename Tin, int D>
+template <int D>
 cudaError_t simt_one(const PrefixPlan &p, const PrefixArgs &a) {
-  auto kern = prefix_simt_kernel<Tin, D>;
+  auto kern = prefix_simt_kernel<D>;
   constexpr int smem = SimtLayout<D>::bytes;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   unsigned char *ws = static_cast<unsigned char *>(a.ws);
-  return launch_pdl(kern, dim3(p.grid), dim3(kSThreads), smem, a.stream, static_cast<const Tin *>(a.q),
-                    static_cast<const Tin *>(a.k), static_cast<const Tin *>(a.v), a.prefix_len, a.head_stride,
+  return launch_pdl(kern, dim3(p.grid), dim3(kSThreads), smem, a.stream, static_cast<const float *>(a.q),
+                    static_cast<const float *>(a.k), static_cast<const float *>(a.v), a.prefix_len, a.head_stride,
                     a.sm_scale * kLog2e, p.g, reinterpret_cast<float *>(ws + p.off_part_o),
                     reinterpret_cast<float *>(ws + p.off_part_l), static_cast<WsHeader *>(a.ws));
 }
 
 }  // namespace
 
-cudaError_t launch_prefix_simt(const PrefixPlan &p, const PrefixArgs &a, int in_f32) {
-  if (in_f32) return p.g.D == 128 ? simt_one<float, 128>(p, a) : simt_one<float, 64>(p, a);
-  return p.g.D == 128 ? simt_one<__nv_bfloat16, 128>(p, a) : simt_one<__nv_bfloat16, 64>(p, a);
+cudaError_t launch_prefix_simt(const PrefixPlan &p, const PrefixArgs &a) {
+  return p.g.D == 128 ? simt_one<128>(p, a) : simt_one<64>(p, a);
 }
 
 cudaError_t launch_prefix_merge(const PrefixPlan &p, const PrefixArgs &a) {
@@ -279,7 +269,6 @@ cudaError_t launch_prefix_merge(const PrefixPlan &p, const PrefixArgs &a) {
 }
 
 PrefixPlan plan_prefix(int B, int T, int Hq, int Hkv, int D, int prefix_cap, int kv_cap, int in_f32, int sm_count) {
-  (void)in_f32;
   PrefixPlan p{};
   PrefixGeom &g = p.g;
   g.B = B;
@@ -290,14 +279,14 @@ PrefixPlan plan_prefix(int B, int T, int Hq, int Hkv, int D, int prefix_cap, int
   g.G = Hq / Hkv;
   g.R = B * T * g.G;
   g.prefix_cap = prefix_cap;
-  g.tile_rows = kSRows;
-  g.key_tile = kSKeys;
-  g.last_half = 0;
+  g.tile_rows = in_f32 ? kSRows : 256;
+  g.key_tile = in_f32 ? kSKeys : 128;
   g.RT = (g.R + g.tile_rows - 1) / g.tile_rows;
+  g.last_half = !in_f32 && g.R - (g.RT - 1) * g.tile_rows <= 128;
   g.slot_rows = std::min(g.tile_rows, g.R);
   p.own = plan_attention(B, T, Hq, Hkv, D, kv_cap, sm_count);
   p.own_cap = kv_cap;
-  p.grid = 2 * sm_count;  // resident CTAs: two of 116 KB shared memory an SM at D = 128
+  p.grid = in_f32 ? 2 * sm_count : sm_count;  // the CTAs that fit: two of 116 KB shared memory an SM, one of 226 KB
   const size_t rows = static_cast<size_t>(B) * T * Hq;
   const size_t slots = static_cast<size_t>(p.grid) + static_cast<size_t>(Hkv) * g.RT;
   size_t off = align_up(p.own.ws_bytes);  // the own attention's scratch (and the header) comes first

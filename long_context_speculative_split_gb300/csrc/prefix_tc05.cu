@@ -103,6 +103,16 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
 __device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
+// True in one lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t e;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(e));
+  return e != 0;
+}
 // D[128 x N] (+)= A[128 x 16] B[16 x N] with A (float16 pairs) in tensor memory.
 __device__ __forceinline__ void umma_f16_ts(uint32_t dtmem, uint32_t atmem, uint64_t bdesc, uint32_t idesc,
                                             uint32_t accumulate) {
@@ -137,6 +147,11 @@ __device__ __forceinline__ bool wait_or_abort(uint64_t *bar, uint32_t parity, Ws
   raise_error_sr(hdr, 0x8u);
   *abort_flag = 1;
   return false;
+}
+
+// The same for a whole warp, which goes on or gives up together.
+__device__ __forceinline__ bool all_wait(uint64_t *bar, uint32_t parity, WsHeader *hdr, volatile int *abort_flag) {
+  return __all_sync(0xffffffffu, wait_or_abort(bar, parity, hdr, abort_flag));
 }
 
 // P = 2^(s * s2 - mu) of one row's 128 scores into tensor memory as float16 pairs, 32 keys a store;
@@ -246,64 +261,82 @@ __global__ void __launch_bounds__(kPThreads, 1)
 
   if (warp >= 12) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 32;");
-    if (warp == 12 && lane == 0) {
+    if (warp == 12) {
       // ------------------------------------------------------------------ MMA issue
+      // The whole warp walks the steps and one elected lane issues: in a branch that the
+      // compiler takes for divergent, an MMA costs about 100 clocks to issue.
       constexpr uint32_t kIdescS = umma_idesc_bf16(kPRows, kPKeys);
       constexpr uint32_t kIdescO = umma_idesc_f16_bt(kPRows, D);
-      const uint32_t q_base = smem_addr(smem + Lay::off_q), k_base = smem_addr(smem + Lay::off_k),
-                     v_base = smem_addr(smem + Lay::off_v);
-      uint32_t kc = 0, vc = 0, pc[2] = {0, 0};  // K tiles and V tiles used, P tiles taken per slot
+      const uint64_t q_desc = umma_desc(smem_addr(smem + Lay::off_q)), k_desc = umma_desc(smem_addr(smem + Lay::off_k)),
+                     v_desc = umma_desc_v(smem_addr(smem + Lay::off_v));
+      uint32_t ks = 0, kph = 0, vs = 0, vph = 0;  // stage and parity of the K and V tile in use
+      uint32_t ppar = 0;                          // parity of the next P tile (the same for both slots)
       uint32_t segs = 0;
       bool ok = true;
       while (x < x1 && ok) {
         const PSeg sg = next_seg(p.g, line, x, x1);
+        // O_w (+)= P_w V
         auto pv = [&](int s, int w) {
-          const uint32_t st = vc % VS;
-          if (!wait_or_abort(&p_full[w], pc[w]++ & 1u, hdr, abort_flag)) return false;
-          if ((w == 0 || !sg.dual) && !wait_or_abort(&v_full[st], (vc / VS) & 1u, hdr, abort_flag)) return false;
-          if (s == 0 && segs > 0 && !wait_or_abort(&o_free[w], (segs - 1) & 1u, hdr, abort_flag)) return false;
+          if (!all_wait(&p_full[w], ppar, hdr, abort_flag)) return false;
+          if ((w == 0 || !sg.dual) && !all_wait(&v_full[vs], vph, hdr, abort_flag)) return false;
+          if (s == 0 && segs > 0 && !all_wait(&o_free[w], (segs - 1) & 1u, hdr, abort_flag)) return false;
           tc_fence_after();
-          const uint32_t vt = v_base + st * Lay::kTile;
+          const uint64_t vd = v_desc + static_cast<uint64_t>(vs * (Lay::kTile >> 4));
+          const bool last_use = w == 1 || !sg.dual;
+          if (elect_one()) {
 #pragma unroll
-          for (int kk = 0; kk < kPKeys / 16; ++kk)
-            umma_f16_ts(tmem + 256 + w * D, tmem + w * 128 + kk * 8, umma_desc_v(vt + kk * 2048), kIdescO,
-                        (s > 0 || kk > 0) ? 1u : 0u);
-          if (w == 1 || !sg.dual) {
-            umma_commit(&v_empty[st]);
-            ++vc;
+            for (int kk = 0; kk < kPKeys / 16; ++kk)
+              umma_f16_ts(tmem + 256 + w * D, tmem + w * 128 + kk * 8, vd + kk * (2048 >> 4), kIdescO,
+                          (s > 0 || kk > 0) ? 1u : 0u);
+            if (last_use) umma_commit(&v_empty[vs]);
+          }
+          __syncwarp();
+          if (last_use && ++vs == VS) {
+            vs = 0;
+            vph ^= 1u;
           }
           return true;
         };
-        if (!(ok = wait_or_abort(q_full, segs & 1u, hdr, abort_flag))) break;
+        if (!(ok = all_wait(q_full, segs & 1u, hdr, abort_flag))) break;
         for (int s = 0; s < sg.n && ok; ++s) {
           for (int w = 0; w < 2 && ok; ++w) {
             if (s > 0 && !(ok = pv(s - 1, w))) break;
-            const uint32_t st = kc % KS;
-            if ((w == 0 || !sg.dual) && !(ok = wait_or_abort(&k_full[st], (kc / KS) & 1u, hdr, abort_flag))) break;
+            if ((w == 0 || !sg.dual) && !(ok = all_wait(&k_full[ks], kph, hdr, abort_flag))) break;
             tc_fence_after();
-            const uint32_t qt = q_base + (sg.dual ? w * Lay::kTile : 0), kt = k_base + st * Lay::kTile;
+            const uint64_t qd = q_desc + static_cast<uint64_t>((sg.dual ? w : 0) * (Lay::kTile >> 4));
+            const uint64_t kd = k_desc + static_cast<uint64_t>(ks * (Lay::kTile >> 4));
+            const bool last_use = w == 1 || !sg.dual;
+            if (elect_one()) {
 #pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk) {
-              const uint32_t off = (kk >> 2) * Lay::kHalf + (kk & 3) * 32;
-              umma_f16(tmem + w * 128, umma_desc(qt + off), umma_desc(kt + off), kIdescS, kk > 0 ? 1u : 0u);
+              for (int kk = 0; kk < D / 16; ++kk) {
+                const uint64_t off = ((kk >> 2) * Lay::kHalf + (kk & 3) * 32) >> 4;
+                umma_f16(tmem + w * 128, qd + off, kd + off, kIdescS, kk > 0 ? 1u : 0u);
+              }
+              if (last_use) umma_commit(&k_empty[ks]);
+              umma_commit(&s_full[w]);
             }
-            if (w == 1 || !sg.dual) {
-              umma_commit(&k_empty[st]);
-              ++kc;
+            __syncwarp();
+            if (last_use && ++ks == KS) {
+              ks = 0;
+              kph ^= 1u;
             }
-            umma_commit(&s_full[w]);
           }
+          if (s > 0) ppar ^= 1u;
         }
         if (!ok) break;
-        umma_commit(q_empty);
+        if (elect_one()) umma_commit(q_empty);
+        __syncwarp();
         for (int w = 0; w < 2 && ok; ++w) {
           ok = pv(sg.n - 1, w);
-          if (ok) umma_commit(&o_done[w]);
+          if (ok && elect_one()) umma_commit(&o_done[w]);
+          __syncwarp();
         }
+        ppar ^= 1u;
         ++segs;
         x += sg.n;
       }
-      umma_commit(mma_done);
+      if (elect_one()) umma_commit(mma_done);
+      __syncwarp();
       mbar_wait(mma_done, 0);
     } else if (warp == 13 && lane == 0) {
       // ------------------------------------------------------------------ K tiles
@@ -353,7 +386,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
         }
       };
       // query rows, zero past the last; a negative scale turns their sign
-      ok = __all_sync(0xffffffffu, segs == 0 || wait_or_abort(q_empty, (segs - 1) & 1u, hdr, abort_flag));
+      ok = segs == 0 || all_wait(q_empty, (segs - 1) & 1u, hdr, abort_flag);
       if (!ok) break;
       for (int w = 0; w < (sg.dual ? 2 : 1); ++w) {
 #pragma unroll
@@ -382,7 +415,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
       fetch(0);
       for (int i = 0; i < tiles; ++i) {
         const uint32_t st = vc % VS;
-        ok = __all_sync(0xffffffffu, wait_or_abort(&v_empty[st], ((vc / VS) & 1u) ^ 1u, hdr, abort_flag));
+        ok = all_wait(&v_empty[st], ((vc / VS) & 1u) ^ 1u, hdr, abort_flag);
         if (!ok) break;
         unsigned char *vt = smem + Lay::off_v + st * Lay::kTile + half_off;
 #pragma unroll
@@ -418,7 +451,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
       float m = -INFINITY, l = 0.f;  // m: what P and O are scaled by (in units of log2)
       for (int s = 0; s < sg.n; ++s) {
         // tensor memory accesses are warp-collective: a warp skips a tile only as a whole
-        if (!__all_sync(0xffffffffu, wait_or_abort(&s_full[w], sc++ & 1u, hdr, abort_flag))) continue;
+        if (!all_wait(&s_full[w], sc++ & 1u, hdr, abort_flag)) continue;
         tc_fence_after();
         const int tile = sg.dual ? sg.first + s : 2 * (sg.first + s) + w;
         const int nk = plen - tile * kPKeys;  // keys of this tile; zero or less: none
@@ -468,7 +501,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
         if (lane == 0) mbar_arrive(&p_full[w]);
       }
       // ---- end of the segment: this CTA's partial result of the pair
-      const bool got = __all_sync(0xffffffffu, wait_or_abort(&o_done[w], segs & 1u, hdr, abort_flag));
+      const bool got = all_wait(&o_done[w], segs & 1u, hdr, abort_flag);
       tc_fence_after();
       if (!sg.dual) {  // both slots hold the same rows: slot 0 joins slot 1's result to its own
         if (w == 1) sm_ml[tl] = make_float2(m, l);

@@ -140,17 +140,18 @@ int current_sm_count() {
 }
 
 int encode_kv_tensor_map(CUtensorMap *map, const void *base, int B, int Hkv, int kv_cap, int D,
-                         int64_t batch_stride, int64_t head_stride, unsigned box_rows) {
+                         int64_t batch_stride, int64_t head_stride, unsigned box_rows, unsigned box_cols) {
   EncodeFn fn = encode_fn();
   if (!fn) return -1;
   const cuuint64_t dims[4] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(kv_cap),
                               static_cast<cuuint64_t>(Hkv), static_cast<cuuint64_t>(B)};
   const cuuint64_t strides[3] = {static_cast<cuuint64_t>(D) * 2, static_cast<cuuint64_t>(head_stride) * 2,
                                  static_cast<cuuint64_t>(batch_stride) * 2};
-  const cuuint32_t box[4] = {64, box_rows, 1, 1};
+  const cuuint32_t box[4] = {box_cols, box_rows, 1, 1};
   const cuuint32_t estr[4] = {1, 1, 1, 1};
   CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(base), dims, strides, box, estr,
-                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, box_cols == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return static_cast<int>(r);
 }
@@ -512,7 +513,7 @@ mgd_status mgd_prefix_attn(const void *q, const void *k_prefix, const void *v_pr
   if (static_cast<int64_t>(B) * T * Hq > INT32_MAX)
     return fail(MGD_ERR_UNSUPPORTED, "B * T * Hq must be below 2^31");
   const int in_f32 = in_dtype == MGD_F32;
-  const PrefixPlan plan = plan_prefix(B, T, Hq, Hkv, D, prefix_cap, kv_cap, in_f32, current_sm_count());
+  PrefixPlan plan = plan_prefix(B, T, Hq, Hkv, D, prefix_cap, kv_cap, in_f32, current_sm_count());
   if (ws_bytes < plan.ws_bytes) return fail(MGD_ERR_WORKSPACE, "workspace %zu < %zu bytes", ws_bytes, plan.ws_bytes);
   if (static_cast<int64_t>(plan.g.RT) * Hkv * ((prefix_cap + plan.g.key_tile - 1) / plan.g.key_tile) > INT32_MAX)
     return fail(MGD_ERR_UNSUPPORTED, "too many rows and prefix keys for one call");
@@ -541,10 +542,14 @@ mgd_status mgd_prefix_attn(const void *q, const void *k_prefix, const void *v_pr
     if ((s = own()) != MGD_OK) return s;
     e = launch_prefix_simt(plan, a);
   } else {
-    CUtensorMap km;
-    if (encode_kv_tensor_map(&km, k_prefix, 1, Hkv, prefix_cap, D, prefix_head_stride * Hkv, prefix_head_stride, 128) != 0)
+    // each CTA of a pair loads half of a key tile's keys of K and half of its columns of V
+    CUtensorMap km, vm;
+    if (encode_kv_tensor_map(&km, k_prefix, 1, Hkv, prefix_cap, D, prefix_head_stride * Hkv, prefix_head_stride) != 0 ||
+        encode_kv_tensor_map(&vm, v_prefix, 1, Hkv, prefix_cap, D, prefix_head_stride * Hkv, prefix_head_stride, 128,
+                             D / 2) != 0)
       return fail(MGD_ERR_CUDA, "cuTensorMapEncodeTiled failed");
-    e = launch_prefix_tc05(plan, a, km);
+    plan.grid = prefix_tc05_clusters(D, plan.grid);
+    e = launch_prefix_tc05(plan, a, km, vm);
     if (e == cudaSuccess && (s = own()) != MGD_OK) return s;
   }
   if (e != cudaSuccess) return cuda_fail(e, "prefix attention launch");

@@ -97,10 +97,10 @@ size_t simt_attention_ws_bytes();
 cudaError_t launch_attention_simt(const AttnPlan &p, const AttnArgs &a);
 
 // Encode a 4-D bf16 tensor map over a KV tensor [B, Hkv, kv_cap, D] with
-// boxes of 64 columns x box_rows rows and 128-byte swizzling.  Returns a CUDA
-// driver status.
+// boxes of box_cols (64 or 32) columns x box_rows rows, swizzled over the box's
+// width.  Returns a CUDA driver status.
 int encode_kv_tensor_map(CUtensorMap *map, const void *base, int B, int Hkv, int kv_cap, int D,
-                         int64_t batch_stride, int64_t head_stride, unsigned box_rows = 64);
+                         int64_t batch_stride, int64_t head_stride, unsigned box_rows = 64, unsigned box_cols = 64);
 
 // ------------------------------------------------------------------ shared prefix
 // Rows and steps of the attention over a prefix that every sequence of the batch
@@ -118,7 +118,7 @@ struct PrefixGeom {
 struct PrefixPlan {
   PrefixGeom g;
   AttnPlan own;     // attention over each sequence's own cache
-  int own_cap, grid;  // grid: CTAs of the prefix kernel
+  int own_cap, grid;  // grid: CTAs of the float32 prefix kernel, clusters of the bf16 one
   size_t off_own_o, off_own_l;    // float [B][T][Hq][D], [B][T][Hq]
   size_t off_part_o, off_part_l;  // float [slots][slot_rows][D], [slots][slot_rows]
   size_t ws_bytes;
@@ -139,7 +139,9 @@ struct PrefixArgs {
   cudaStream_t stream;
 };
 // Partial results over the prefix, and their merge with the own-cache results.
-cudaError_t launch_prefix_tc05(const PrefixPlan &p, const PrefixArgs &a, const CUtensorMap &kmap);  // bf16
+int prefix_tc05_clusters(int D, int most);  // clusters of the bf16 kernel that run at once on the current device
+cudaError_t launch_prefix_tc05(const PrefixPlan &p, const PrefixArgs &a, const CUtensorMap &kmap,
+                               const CUtensorMap &vmap);                  // bf16
 cudaError_t launch_prefix_simt(const PrefixPlan &p, const PrefixArgs &a);                           // float32
 cudaError_t launch_prefix_merge(const PrefixPlan &p, const PrefixArgs &a);
 

@@ -279,14 +279,15 @@ PrefixPlan plan_prefix(int B, int T, int Hq, int Hkv, int D, int prefix_cap, int
   g.G = Hq / Hkv;
   g.R = B * T * g.G;
   g.prefix_cap = prefix_cap;
-  g.tile_rows = in_f32 ? kSRows : 256;
+  g.tile_rows = in_f32 ? kSRows : 512;
   g.key_tile = in_f32 ? kSKeys : 128;
   g.RT = (g.R + g.tile_rows - 1) / g.tile_rows;
-  g.last_half = !in_f32 && g.R - (g.RT - 1) * g.tile_rows <= 128;
+  g.last_half = !in_f32 && g.R - (g.RT - 1) * g.tile_rows <= 256;
   g.slot_rows = std::min(g.tile_rows, g.R);
   p.own = plan_attention(B, T, Hq, Hkv, D, kv_cap, sm_count);
   p.own_cap = kv_cap;
-  p.grid = in_f32 ? 2 * sm_count : sm_count;  // the CTAs that fit: two of 116 KB shared memory an SM, one of 226 KB
+  // what fits at once: two CTAs of 116 KB shared memory an SM; clusters of two CTAs of 226 KB
+  p.grid = in_f32 ? 2 * sm_count : std::max(1, sm_count / 2);
   const size_t rows = static_cast<size_t>(B) * T * Hq;
   const size_t slots = static_cast<size_t>(p.grid) + static_cast<size_t>(Hkv) * g.RT;
   size_t off = align_up(p.own.ws_bytes);  // the own attention's scratch (and the header) comes first

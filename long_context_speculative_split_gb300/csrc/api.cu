@@ -156,14 +156,14 @@ int encode_kv_tensor_map(CUtensorMap *map, const void *base, int B, int Hkv, int
   return static_cast<int>(r);
 }
 
-int encode_qwin_tensor_map(CUtensorMap *map, const void *base, int B, int W, int Hq, int D, int G) {
+int encode_qwin_tensor_map(CUtensorMap *map, const void *base, int B, int W, int Hq, int D, int G, int box_w) {
   EncodeFn fn = encode_fn();
-  if (!fn || G > 256 || W > 256) return -1;
+  if (!fn || G > 256 || box_w > 256) return -1;
   const cuuint64_t dims[4] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(Hq), static_cast<cuuint64_t>(W),
                               static_cast<cuuint64_t>(B)};
   const cuuint64_t strides[3] = {static_cast<cuuint64_t>(D) * 2, static_cast<cuuint64_t>(Hq) * D * 2,
                                  static_cast<cuuint64_t>(W) * Hq * D * 2};
-  const cuuint32_t box[4] = {64, static_cast<cuuint32_t>(G), static_cast<cuuint32_t>(W), 1};
+  const cuuint32_t box[4] = {64, static_cast<cuuint32_t>(G), static_cast<cuuint32_t>(box_w), 1};
   const cuuint32_t estr[4] = {1, 1, 1, 1};
   CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(base), dims, strides, box, estr,
                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -316,7 +316,7 @@ static mgd_status run_snapkv(const void *q_win, const void *k, const void *v, co
     // take 64-row boxes
     CUtensorMap km128;
     const bool tc05 = snap_tc05_eligible(plan) && sm_scale > 0.f &&
-                      encode_qwin_tensor_map(&qm, q_win, B, W, Hq, D, Hq / Hkv) == 0 &&
+                      encode_qwin_tensor_map(&qm, q_win, B, W, Hq, D, Hq / Hkv, W) == 0 &&
                       encode_kv_tensor_map(&km128, k, B, Hkv, kv_cap, D, kv_batch_stride, kv_head_stride, 128) == 0;
     e = launch_snapkv(plan, a, 0, tc05 ? &km128 : &km, tc05 ? &qm : nullptr);
   } else {
@@ -548,8 +548,12 @@ mgd_status mgd_prefix_attn(const void *q, const void *k_prefix, const void *v_pr
         encode_kv_tensor_map(&vm, v_prefix, 1, Hkv, prefix_cap, D, prefix_head_stride * Hkv, prefix_head_stride, 128,
                              D / 2) != 0)
       return fail(MGD_ERR_CUDA, "cuTensorMapEncodeTiled failed");
+    CUtensorMap qm;
+    const int G = Hq / Hkv;
+    const bool q_tma = 128 % G == 0 && sm_scale >= 0.f &&
+                       encode_qwin_tensor_map(&qm, q, 1, B * T, Hq, D, G, 128 / G) == 0;
     plan.grid = prefix_tc05_clusters(D, plan.grid);
-    e = launch_prefix_tc05(plan, a, km, vm);
+    e = launch_prefix_tc05(plan, a, km, vm, q_tma ? &qm : nullptr);
     if (e == cudaSuccess && (s = own()) != MGD_OK) return s;
   }
   if (e != cudaSuccess) return cuda_fail(e, "prefix attention launch");

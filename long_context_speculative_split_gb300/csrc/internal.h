@@ -141,7 +141,7 @@ struct PrefixArgs {
 // Partial results over the prefix, and their merge with the own-cache results.
 int prefix_tc05_clusters(int D, int most);  // clusters of the bf16 kernel that run at once on the current device
 cudaError_t launch_prefix_tc05(const PrefixPlan &p, const PrefixArgs &a, const CUtensorMap &kmap,
-                               const CUtensorMap &vmap);                  // bf16
+                               const CUtensorMap &vmap, const CUtensorMap *qmap);  // bf16; qmap nullable
 cudaError_t launch_prefix_simt(const PrefixPlan &p, const PrefixArgs &a);                           // float32
 cudaError_t launch_prefix_merge(const PrefixPlan &p, const PrefixArgs &a);
 
@@ -193,8 +193,8 @@ bool snap_tc05_eligible(const SnapPlan &p);
 cudaError_t launch_snap_score_tc05(const SnapPlan &p, const SnapArgs &a, const CUtensorMap &kmap,
                                    const CUtensorMap &qmap);
 // 4-D bf16 tensor map over window queries [B, W, Hq, D] with one box per
-// (64 columns, G heads, W rows): the 128-byte-swizzled W*G x 64 tile of a KV head.
-int encode_qwin_tensor_map(CUtensorMap *map, const void *base, int B, int W, int Hq, int D, int G);
+// (64 columns, G heads, box_w of the W rows): the 128-byte-swizzled box_w*G x 64 tile of a KV head.
+int encode_qwin_tensor_map(CUtensorMap *map, const void *base, int B, int W, int Hq, int D, int G, int box_w);
 
 // ------------------------------------------------------------------ self-test
 // One bounded wait that nothing completes (0: an mbarrier phase, 1: a counter

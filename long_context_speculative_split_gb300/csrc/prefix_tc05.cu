@@ -25,8 +25,8 @@
 // means rescaling O_w in tensor memory.  The sum of exponentials is kept in float32,
 // unrounded.
 //
-// Roles (16 warps a CTA): 0-3 and 4-7 softmax of slot 0 / 1, 8-11 query rows and V's conversion,
-// 12 MMA issue (of the first CTA), 13 K and V tiles by TMA.  Registers a thread: 184, 88 and 56
+// Roles (16 warps a CTA): 0-3 and 4-7 softmax of slot 0 / 1, 8-11 V's conversion,
+// 12 MMA issue (of the first CTA), 13 query rows, K and V tiles by TMA.  Registers a thread: 184, 88 and 56
 // for the three kinds of warp group (2 * 184 + 88 + 56 = 4 * 128, the launch's own total).
 #include <cuda_fp16.h>
 
@@ -72,6 +72,10 @@ struct PParams {
   PrefixGeom g;
   float sl2;      // |scale| * log2(e); the sign goes into the query rows
   uint32_t flip;  // 0x80008000 when the scale is negative
+  // Query rows by TMA: boxes of whole groups of G heads, so 128 has to be a multiple of G, and the rows
+  // stay as they are, so the scale must not be negative.  Else four warps gather them: 5.6 us instead
+  // of 2.1 until the first two blocks are there at 512 rows a KV head.
+  int q_tma;
 };
 
 // This CTA's next run of steps within one pair.
@@ -320,7 +324,7 @@ __device__ __forceinline__ void st_f8(float *p, const float (&v)[8]) {
 template <int D>
 __global__ void __launch_bounds__(kPThreads, 1)
     prefix_tc05_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
-                       const __nv_bfloat16 *__restrict__ q, const int32_t *__restrict__ prefix_len,
+                       const __grid_constant__ CUtensorMap qmap, const __nv_bfloat16 *__restrict__ q, const int32_t *__restrict__ prefix_len,
                        float *__restrict__ part_o, float *__restrict__ part_l, WsHeader *hdr, PParams p) {
   using Lay = PLayout<D>;
   constexpr int NS = Lay::kStages;
@@ -356,7 +360,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
       mbar_init(&v_full[i], 8);
       mbar_init(&v_empty[i], 1);
     }
-    mbar_init(q_full, 8);
+    mbar_init(q_full, p.q_tma ? 1 : 8);
     mbar_init(q_empty, 1);
     for (int w = 0; w < 2; ++w) {
       mbar_init(&s_full[w], 1);
@@ -462,12 +466,23 @@ __global__ void __launch_bounds__(kPThreads, 1)
       // ------------------------------------------------------------------ K tiles
       tma_prefetch_desc(&kmap);
       tma_prefetch_desc(&vmap);
-      uint32_t n = 0;  // tiles issued
+      if (p.q_tma) tma_prefetch_desc(&qmap);
+      uint32_t n = 0, segs = 0;  // tiles issued, query blocks issued
       Ring<NS> r;
       bool ok = true;
       while (x < x1 && ok) {
         const PSeg sg = next_seg(p.g, line, x, x1);
         const int per = sg.dual ? 1 : 2;
+        if (p.q_tma) {
+          if (segs > 0 && !(ok = wait_or_abort(q_empty, (segs - 1) & 1u, hdr, abort_flag))) break;
+          const int blocks = sg.dual ? 2 : 1;
+          if (rank == 0) mbar_arrive_expect_tx(q_full, 2 * blocks * Lay::kQTile);
+          for (int w = 0; w < blocks; ++w)
+            for (int hf = 0; hf < D / 64; ++hf)
+              tma2_load_4d(smem + Lay::off_q + w * Lay::kQTile + hf * Lay::kHalf, &qmap, in_first_cta(q_full), 64 * hf,
+                           sg.h * p.g.G, (sg.rt * p.g.tile_rows + w * 256 + rank * 128) / p.g.G, 0);
+          ++segs;
+        }
         for (int i = 0; i < sg.n * per; ++i) {
           const int key0 = (sg.first * per + i) * kPKeys;
           if (!(ok = wait_or_abort(&k_empty[r.stage], r.parity ^ 1u, hdr, abort_flag))) break;
@@ -484,7 +499,8 @@ __global__ void __launch_bounds__(kPThreads, 1)
         }
         x += sg.n;
       }
-      // every copy issued has landed (the K of both CTAs counts in the first) before the CTAs end
+      // every copy issued has landed (Q and K of both CTAs count in the first) before the CTAs end
+      if (rank == 0 && segs > 0) mbar_wait(q_full, (segs - 1) & 1u);
       for (uint32_t i = n > NS ? n - NS : 0; i < n; ++i) {
         if (rank == 0) mbar_wait(&k_full[i % NS], (i / NS) & 1u);
         if (ok || i + 1 < n) mbar_wait(&v_land[i % NS], (i / NS) & 1u);
@@ -496,39 +512,52 @@ __global__ void __launch_bounds__(kPThreads, 1)
     constexpr int kChunks = D / 16;              // 16-byte chunks of this CTA's columns of a key
     constexpr int kPer = kChunks;                // chunks of a tile per thread: 128 keys x kChunks / 128
     constexpr int kStep = 128 / kChunks;         // keys between a thread's chunks
-    constexpr int kQChunks = D / 8, kQStep = 128 / kQChunks;
     const int tid = threadIdx.x - 256;
     const int ch = tid % kChunks, r0 = tid / kChunks;
+    constexpr int kQPer = D / 8, kQStep = 128 / kQPer;  // 16-byte chunks of a query row; rows between a thread's
+    const int qc = tid % kQPer, qr = tid / kQPer;
+    const int step_bt = kQStep / p.g.G, step_g = kQStep % p.g.G;
     Ring<NS> vr;
     uint32_t segs = 0;
     bool ok = true;
     while (x < x1 && ok) {
       const PSeg sg = next_seg(p.g, line, x, x1);
       const int per = sg.dual ? 1 : 2, tiles = sg.n * per;
-      // query rows, zero past the last; a negative scale turns their sign
-      if (segs > 0 && !(ok = all_wait(q_empty, (segs - 1) & 1u, hdr, abort_flag))) break;
-      for (int w = 0; w < (sg.dual ? 2 : 1); ++w) {
-        const int qc = tid % kQChunks, qr = tid / kQChunks;
-#pragma unroll 4
-        for (int j = 0; j < kQChunks; ++j) {
-          const int r = sg.rt * p.g.tile_rows + w * 256 + rank * 128 + qr + j * kQStep;
-          uint4 y = make_uint4(0u, 0u, 0u, 0u);
-          if (r < p.g.R) {
-            const int bt = r / p.g.G, gg = r - bt * p.g.G;
-            y = __ldg(reinterpret_cast<const uint4 *>(q + (static_cast<int64_t>(bt) * p.g.Hq + sg.h * p.g.G + gg) * D +
-                                                      qc * 8));
+      if (!p.q_tma) {
+        // query rows, zero past the last; a negative scale turns their sign.  A thread's rows are kQStep
+        // apart, so its (token, head) pair steps along without divisions.
+        if (segs > 0 && !(ok = all_wait(q_empty, (segs - 1) & 1u, hdr, abort_flag))) break;
+        for (int w = 0; w < (sg.dual ? 2 : 1); ++w) {
+          const int row0 = sg.rt * p.g.tile_rows + w * 256 + rank * 128 + qr;
+          int bt = row0 / p.g.G, gg = row0 - bt * p.g.G;
+          uint4 y[kQPer];
+#pragma unroll
+          for (int j = 0; j < kQPer; ++j) {
+            y[j] = row0 + j * kQStep < p.g.R
+                       ? __ldg(reinterpret_cast<const uint4 *>(
+                             q + (static_cast<int64_t>(bt) * p.g.Hq + sg.h * p.g.G + gg) * D + qc * 8))
+                       : make_uint4(0u, 0u, 0u, 0u);
+            bt += step_bt;
+            gg += step_g;
+            if (gg >= p.g.G) {
+              gg -= p.g.G;
+              ++bt;
+            }
           }
-          y.x ^= p.flip;
-          y.y ^= p.flip;
-          y.z ^= p.flip;
-          y.w ^= p.flip;
-          *reinterpret_cast<uint4 *>(smem + Lay::off_q + w * Lay::kQTile + (qc >> 3) * Lay::kHalf +
-                                     swz128(qr + j * kQStep, qc & 7)) = y;
+#pragma unroll
+          for (int j = 0; j < kQPer; ++j) {
+            y[j].x ^= p.flip;
+            y[j].y ^= p.flip;
+            y[j].z ^= p.flip;
+            y[j].w ^= p.flip;
+            *reinterpret_cast<uint4 *>(smem + Lay::off_q + w * Lay::kQTile + (qc >> 3) * Lay::kHalf +
+                                       swz128(qr + j * kQStep, qc & 7)) = y[j];
+          }
         }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) arrive_first_cta(q_full);
       }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) arrive_first_cta(q_full);
       for (int i = 0; i < tiles; ++i) {
         if (!(ok = all_wait(&v_land[vr.stage], vr.parity, hdr, abort_flag))) break;
         unsigned char *vt = smem + Lay::off_v + vr.stage * Lay::kVTile;
@@ -680,16 +709,18 @@ int clusters(int most) {
 }
 
 template <int D>
-cudaError_t launch_one(const PrefixPlan &pl, const PrefixArgs &a, const CUtensorMap &kmap, const CUtensorMap &vmap) {
+cudaError_t launch_one(const PrefixPlan &pl, const PrefixArgs &a, const CUtensorMap &kmap, const CUtensorMap &vmap,
+                       const CUtensorMap *qmap) {
   cudaError_t e = prepare_kernel<D>();
   if (e != cudaSuccess) return e;
   PParams kp;
   kp.g = pl.g;
   kp.sl2 = fabsf(a.sm_scale) * kLog2e;
   kp.flip = a.sm_scale < 0.f ? 0x80008000u : 0u;
+  kp.q_tma = qmap != nullptr;
   unsigned char *ws = static_cast<unsigned char *>(a.ws);
   return launch_pdl_cluster(prefix_tc05_kernel<D>, dim3(2 * pl.grid), dim3(kPThreads), dim3(2), PLayout<D>::alloc,
-                            a.stream, kmap, vmap, static_cast<const __nv_bfloat16 *>(a.q), a.prefix_len,
+                            a.stream, kmap, vmap, qmap ? *qmap : kmap, static_cast<const __nv_bfloat16 *>(a.q), a.prefix_len,
                             reinterpret_cast<float *>(ws + pl.off_part_o),
                             reinterpret_cast<float *>(ws + pl.off_part_l), static_cast<WsHeader *>(a.ws), kp);
 }
@@ -699,8 +730,8 @@ cudaError_t launch_one(const PrefixPlan &pl, const PrefixArgs &a, const CUtensor
 int prefix_tc05_clusters(int D, int most) { return D == 128 ? clusters<128>(most) : clusters<64>(most); }
 
 cudaError_t launch_prefix_tc05(const PrefixPlan &p, const PrefixArgs &a, const CUtensorMap &kmap,
-                               const CUtensorMap &vmap) {
-  return p.g.D == 128 ? launch_one<128>(p, a, kmap, vmap) : launch_one<64>(p, a, kmap, vmap);
+                               const CUtensorMap &vmap, const CUtensorMap *qmap) {
+  return p.g.D == 128 ? launch_one<128>(p, a, kmap, vmap, qmap) : launch_one<64>(p, a, kmap, vmap, qmap);
 }
 
 }  // namespace mgd

@@ -544,7 +544,7 @@ mgd_status mgd_prefix_attn(const void *q, const void *k_prefix, const void *v_pr
   } else {
     // each CTA of a pair loads half of a key tile's keys of K and half of its columns of V
     CUtensorMap km, vm;
-    if (encode_kv_tensor_map(&km, k_prefix, 1, Hkv, prefix_cap, D, prefix_head_stride * Hkv, prefix_head_stride) != 0 ||
+    if (encode_kv_tensor_map(&km, k_prefix, 1, Hkv, prefix_cap, D, prefix_head_stride * Hkv, prefix_head_stride, 32) != 0 ||
         encode_kv_tensor_map(&vm, v_prefix, 1, Hkv, prefix_cap, D, prefix_head_stride * Hkv, prefix_head_stride, 128,
                              D / 2) != 0)
       return fail(MGD_ERR_CUDA, "cuTensorMapEncodeTiled failed");

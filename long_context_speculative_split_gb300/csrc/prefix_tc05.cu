@@ -4,15 +4,16 @@
 // Two CTAs (a cluster, one CTA per SM) work on 512 query rows as two "slots" of 256:
 // of each slot 128 rows live in either CTA, with their accumulators in its tensor
 // memory and a group of four softmax warps of its own:
-//   S_w = Q_w K^T      tcgen05.mma over both CTAs (256 x 128), operands in shared memory
+//   S_w = Q_w K^T      tcgen05.mma over both CTAs (256 x 64), operands in shared memory
 //   P_w = 2^(S_w * scale*log2(e) - m_w)   float16, written over S_w
 //   O_w += P_w V       tcgen05.mma (256 x D), P_w from tensor memory, V float16
-// Each slot's O_w += P_w V and the next S_w = Q_w K^T are issued together; while one
-// slot's softmax runs the tensor cores work for the other slot, and both slots use a
-// key tile while it is in shared memory.  An MMA over two CTAs takes half of K (64 of a
-// tile's 128 keys) and half of V (D/2 columns) from each: with one CTA the reads of Q, K
-// and V, the TMA's writes of K and the stores of V fill the 128 bytes a clock of shared
-// memory (2640 clocks a tile of 256 rows measured where the MMAs alone need 2048).
+// Tensor memory (512 columns) holds O_w (D each) and two S_w of 64 keys each: while the
+// softmax works on one, the tensor cores take the other's P and put the next S in its
+// place, so neither waits for the other.  (One S_w of 128 keys a slot, the other slot the
+// only overlap: 3900 clocks for 128 keys, of which the MMAs are 2048.)  Both slots use a
+// key tile while it is in shared memory, and an MMA over two CTAs takes half of K (32 of
+// 64 keys) and half of V (D/2 columns) from each: with one CTA the reads of Q, K and V,
+// the TMA's writes and the stores of V fill the 128 bytes a clock of shared memory.
 // A head's last row block may have 256 rows or fewer: then both slots hold the same rows
 // and take alternate key tiles, and their results are joined in tensor memory at the end.
 //
@@ -26,10 +27,8 @@
 // unrounded.
 //
 // Roles (16 warps a CTA): 0-3 and 4-7 softmax of slot 0 / 1, 8-11 V's conversion,
-// 12 MMA issue (of the first CTA), 13 query rows, K and V tiles by TMA.  Registers a thread: 184, 88 and 56
+// 12 and 13 MMA issue for slot 0 / 1 (of the first CTA), 14 query rows, K and V tiles by TMA.  Registers a thread: 184, 88 and 56
 // for the three kinds of warp group (2 * 184 + 88 + 56 = 4 * 128, the launch's own total).
-#include <cuda_fp16.h>
-
 #include <algorithm>
 
 #include "common.cuh"
@@ -50,15 +49,16 @@ template <int D>
 struct PLayout {
   static constexpr int kHalf = 128 * 128;            // 128 rows x 64 16-bit columns, 128-byte swizzled
   static constexpr int kQTile = (D / 64) * kHalf;    // 128 query rows
-  static constexpr int kKHalf = 64 * 128;            // 64 keys x 64 columns
-  static constexpr int kKTile = (D / 64) * kKHalf;   // this CTA's 64 keys of a tile
+  static constexpr int kKHalf = 32 * 128;            // 32 keys x 64 columns
+  static constexpr int kKSub = (D / 64) * kKHalf;    // this CTA's 32 of 64 keys
+  static constexpr int kKTile = 2 * kKSub;
   static constexpr int kVTile = 128 * D;             // 128 keys x this CTA's D/2 columns
   static constexpr int kStages = D == 128 ? 5 : 8;   // of K and of V
   static constexpr int off_q = 0;
   static constexpr int off_k = 2 * kQTile;
   static constexpr int off_v = off_k + kStages * kKTile;
   static constexpr int off_bar = off_v + kStages * kVTile;
-  static constexpr int kBars = 5 * kStages + 11;
+  static constexpr int kBars = 5 * kStages + 13;
   static constexpr int off_tmem = off_bar + kBars * 8;
   static constexpr int off_abort = off_tmem + 8;
   static constexpr int off_ml = off_abort + 8;    // float2 [128]: slot 1's maximum and sum
@@ -66,7 +66,7 @@ struct PLayout {
   static constexpr int alloc = bytes + 1024;      // the base is rounded up to 1024
   static_assert(alloc <= 227 * 1024, "shared memory of one CTA");
 };
-constexpr uint32_t kPTmemCols = 512;  // S_0, S_1 (128 columns each), O_0, O_1 (D each)
+constexpr uint32_t kPTmemCols = 512;  // S of slot 0 and 1 (two of 64 columns each), O_0, O_1 (D each)
 
 struct PParams {
   PrefixGeom g;
@@ -108,10 +108,6 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32
   asm volatile("tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};" ::"r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31]), "r"(taddr)
                : "memory");
 }
-__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
-  asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};" ::"r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(taddr)
-               : "memory");
-}
 __device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
@@ -119,9 +115,16 @@ __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.
 template <int N>
 struct Ring {
   uint32_t stage = 0, parity = 0;
-  __device__ __forceinline__ void advance() {
-    if (++stage == N) {
-      stage = 0;
+  __device__ __forceinline__ void advance(uint32_t by = 1) {  // by < N
+    stage += by;
+    if (stage >= N) {
+      stage -= N;
+      parity ^= 1u;
+    }
+  }
+  __device__ __forceinline__ void retreat() {
+    if (stage-- == 0) {
+      stage = N - 1;
       parity ^= 1u;
     }
   }
@@ -163,6 +166,34 @@ __device__ __forceinline__ void umma2_commit(uint64_t *bar) {
       "h"(static_cast<uint16_t>(3))
       : "memory");
 }
+// kind::f16 with D float32, A and B float16, A along the contraction, B across it.
+__host__ __device__ constexpr uint32_t umma_idesc_f16_bt(uint32_t M, uint32_t N) {
+  return (1u << 4) | (1u << 16) | ((N >> 3) << 17) | ((M >> 4) << 24);
+}
+
+// What the MMA warp of a slot issues for one group of 64 keys (`sub` of a tile): the MMAs' operands differ
+// from the bases by constants, which keeps the issue at about 25 clocks an MMA.
+struct MmaState {
+  uint64_t q_desc, k_desc, v_desc;
+  uint32_t s_tmem, o_tmem;
+};
+template <int D>
+__device__ __forceinline__ void product_pv(const MmaState &st, uint64_t vd, int sub, bool add) {
+#pragma unroll
+  for (int kk = 0; kk < 4; ++kk)
+    umma2_ts(st.o_tmem, st.s_tmem + sub * 64 + kk * 8, vd + ((sub * 64 * D + kk * 16 * D) >> 4),
+             umma_idesc_f16_bt(2 * kPRows, D), (add || kk > 0) ? 1u : 0u);
+}
+template <int D>
+__device__ __forceinline__ void product_qk(const MmaState &st, uint64_t qd, uint64_t kd, int sub) {
+  using Lay = PLayout<D>;
+#pragma unroll
+  for (int kk = 0; kk < D / 16; ++kk)
+    umma2_ss(st.s_tmem + sub * 64, qd + (((kk >> 2) * Lay::kHalf + (kk & 3) * 32) >> 4),
+             kd + ((sub * Lay::kKSub + (kk >> 2) * Lay::kKHalf + (kk & 3) * 32) >> 4), umma_idesc_bf16(2 * kPRows, 64),
+             kk > 0 ? 1u : 0u);
+}
+
 // Descriptor of this CTA's columns of V as the B operand, rows (keys) along the contraction and columns
 // contiguous: rows of 128 bytes (D = 128) or 64 bytes (D = 64), swizzled over their own width, groups of 8
 // rows one after the other.
@@ -181,11 +212,6 @@ template <int D>
 __device__ __forceinline__ uint32_t swz_v(int r, int c) {
   return D == 128 ? swz128(r, c) : static_cast<uint32_t>(r * 64 + ((c ^ ((r >> 1) & 3)) << 4));
 }
-// kind::f16 with D float32, A and B float16, A along the contraction, B across it.
-__host__ __device__ constexpr uint32_t umma_idesc_f16_bt(uint32_t M, uint32_t N) {
-  return (1u << 4) | (1u << 16) | ((N >> 3) << 17) | ((M >> 4) << 24);
-}
-
 __device__ __forceinline__ uint32_t cluster_rank() {
   uint32_t r;
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
@@ -231,86 +257,68 @@ __device__ __forceinline__ bool all_wait(uint64_t *bar, uint32_t parity, WsHeade
   return __all_sync(0xffffffffu, wait_or_abort(bar, parity, hdr, abort_flag));
 }
 
-// One row's scores of a tile: P = 2^(s * sl2 - m) over S as float16 pairs, its float32 sum added to l.
-// The 128 scores come in groups of 32, the next one on its way while one is worked on; a group whose
-// maximum exceeds the row's m by more than 2^kRaise raises m first (to the maximum and 2^kHead), so the
-// maximum of the whole tile is never waited for.  kMask: only the first nk keys count.  A template and
-// not a branch within: the compiler would predicate the selections into every tile.
-template <int D, bool kMask>
-__device__ __forceinline__ void softmax_tile(uint32_t s_addr, uint32_t o_addr, float sl2, int nk, bool first, float &m,
-                                             float &l) {
-  uint32_t sv[2][32];
-  float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-  const float2 s2 = make_float2(sl2, sl2);
-  tmem_ld32(s_addr, sv[0]);
+// One row's scores of a group of 64 keys: P = 2^(s * sl2 - m) over S as float16 pairs, its float32 sum
+// added to l.  A maximum that exceeds the row's m by more than 2^kRaise raises m first (to the maximum
+// and 2^kHead); `settle` waits until the products issued so far are done, so that O can be rescaled.
+// kMask: only the first nk keys count.  A template and not a branch within: the compiler would
+// predicate the selections into every group.
+template <int D, bool kMask, typename Settle>
+__device__ __forceinline__ void softmax_group(uint32_t s_addr, uint32_t o_addr, float sl2, int nk, bool first, float &m,
+                                              float &l, const Settle &settle) {
+  uint32_t x[64];
+  tmem_ld32(s_addr, *reinterpret_cast<uint32_t(*)[32]>(&x[0]));
+  tmem_ld32(s_addr + 32, *reinterpret_cast<uint32_t(*)[32]>(&x[32]));
+  tmem_wait_ld();
+  if constexpr (kMask) {
 #pragma unroll
-  for (int h = 0; h < 4; ++h) {
-    uint32_t(&x)[32] = sv[h & 1];
-    tmem_wait_ld();
-    if (h < 3) tmem_ld32(s_addr + 32 * (h + 1), sv[(h + 1) & 1]);  // P only reaches columns read before
-    if constexpr (kMask) {
+    for (int c = 0; c < 64; ++c)
+      if (c >= nk) x[c] = 0xFF800000u;  // -inf
+  }
+  float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-      for (int c = 0; c < 32; ++c)
-        if (32 * h + c >= nk) x[c] = 0xFF800000u;  // -inf
-    }
-    float mx[2] = {-INFINITY, -INFINITY};
+  for (int c = 0; c < 64; c += 8)
 #pragma unroll
-    for (int c = 0; c < 32; c += 4) {
-      mx[0] = fmax3(mx[0], __uint_as_float(x[c]), __uint_as_float(x[c + 1]));
-      mx[1] = fmax3(mx[1], __uint_as_float(x[c + 2]), __uint_as_float(x[c + 3]));
-    }
-    const float top = fmaxf(mx[0], mx[1]);
-    // a row whose every score is -inf so far keeps m = -inf and subtracts 0 instead
-    const float mt = top == -INFINITY ? -INFINITY : top * sl2;
-    const bool raise = mt > m + kRaise || (m == -INFINITY && mt > -INFINITY);
-    if (__any_sync(0xffffffffu, raise)) {
-      const float mn = raise ? mt + kHead : m;
-      const float alpha = raise ? ex2(m - mn) : 1.f;  // m == -inf: 0, nothing is there yet
-      m = mn;
-      l *= alpha;
-      sum[0] = __fmul2_rn(sum[0], make_float2(alpha, alpha));
-      sum[1] = __fmul2_rn(sum[1], make_float2(alpha, alpha));
-      uint32_t o[32];
-#pragma unroll
-      for (int i = 0; i < (h + 1) / 2; ++i) {  // the P of this tile's groups before this one
-        tmem_wait_st();
-        tmem_ld32(s_addr + 32 * i, o);
+    for (int i = 0; i < 4; ++i)
+      mx[i] = fmax3(mx[i], __uint_as_float(x[c + 2 * i]), __uint_as_float(x[c + 2 * i + 1]));
+  const float top = fmaxf(fmax3(mx[0], mx[1], mx[2]), mx[3]);
+  // a row whose every score is -inf so far keeps m = -inf and subtracts 0 instead
+  const float mt = top == -INFINITY ? -INFINITY : top * sl2;
+  const bool raise = mt > m + kRaise || (m == -INFINITY && mt > -INFINITY);
+  if (__any_sync(0xffffffffu, raise)) {
+    const float mn = raise ? mt + kHead : m;
+    const float alpha = raise ? ex2(m - mn) : 1.f;  // m == -inf: 0, nothing is there yet
+    m = mn;
+    l *= alpha;
+    if (!first && settle()) {
+#pragma unroll 1
+      for (int c = 0; c < D; c += 64) {
+        uint32_t o[64];
+        tmem_ld32(o_addr + c, *reinterpret_cast<uint32_t(*)[32]>(&o[0]));
+        tmem_ld32(o_addr + c + 32, *reinterpret_cast<uint32_t(*)[32]>(&o[32]));
         tmem_wait_ld();
 #pragma unroll
-        for (int e = 0; e < 32; ++e)
-          if (32 * i + e < 16 * h) {
-            const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&o[e]));
-            o[e] = pack_f16(f.x * alpha, f.y * alpha);
-          }
-        tmem_st32(s_addr + 32 * i, o);  // columns past the P are S that is read already: they go back as they were
-      }
-      if (!first) {  // S of this step written means that every earlier product is done
-#pragma unroll 1
-        for (int c = 0; c < D; c += 32) {
-          tmem_ld32(o_addr + c, o);
-          tmem_wait_ld();
-#pragma unroll
-          for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
-          tmem_st32(o_addr + c, o);
-        }
+        for (int e = 0; e < 64; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+        tmem_st32(o_addr + c, *reinterpret_cast<const uint32_t(*)[32]>(&o[0]));
+        tmem_st32(o_addr + c + 32, *reinterpret_cast<const uint32_t(*)[32]>(&o[32]));
       }
     }
-    const float mu = m == -INFINITY ? 0.f : m;
-    const float2 nm = make_float2(-mu, -mu);
-    uint32_t pk[16];
-#pragma unroll
-    for (int c = 0; c < 32; c += 2) {
-      const float2 y = __ffma2_rn(make_float2(__uint_as_float(x[c]), __uint_as_float(x[c + 1])), s2, nm);
-      float a = ex2(y.x), b = ex2(y.y);
-      if constexpr (kMask) {  // by place: with a scale of 0 the product of a masked score is NaN
-        a = 32 * h + c < nk ? a : 0.f;
-        b = 32 * h + c + 1 < nk ? b : 0.f;
-      }
-      sum[(c >> 1) & 1] = __fadd2_rn(sum[(c >> 1) & 1], make_float2(a, b));
-      pk[c >> 1] = pack_f16(a, b);
-    }
-    tmem_st16(s_addr + 16 * h, pk);
   }
+  const float mu = m == -INFINITY ? 0.f : m;
+  const float2 s2 = make_float2(sl2, sl2), nm = make_float2(-mu, -mu);
+  float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+  uint32_t pk[32];
+#pragma unroll
+  for (int c = 0; c < 64; c += 2) {
+    const float2 y = __ffma2_rn(make_float2(__uint_as_float(x[c]), __uint_as_float(x[c + 1])), s2, nm);
+    float a = ex2(y.x), b = ex2(y.y);
+    if constexpr (kMask) {  // by place: with a scale of 0 the product of a masked score is NaN
+      a = c < nk ? a : 0.f;
+      b = c + 1 < nk ? b : 0.f;
+    }
+    sum[(c >> 1) & 1] = __fadd2_rn(sum[(c >> 1) & 1], make_float2(a, b));
+    pk[c >> 1] = pack_f16(a, b);
+  }
+  tmem_st32(s_addr, pk);
   l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
 }
 
@@ -339,12 +347,11 @@ __global__ void __launch_bounds__(kPThreads, 1)
   uint64_t *v_empty = v_full + NS;   // [NS] its products are done
   uint64_t *q_full = v_empty + NS;   // query rows of the segment stored (first CTA)
   uint64_t *q_empty = q_full + 1;    // every S product of the segment done
-  uint64_t *s_full = q_empty + 1;    // [2] S of a slot written (and every earlier product done)
-  uint64_t *p_full = s_full + 2;     // [2] P of a slot written (first CTA)
-  uint64_t *o_done = p_full + 2;     // [2] a slot's last product of the segment done
-  uint64_t *o_free = o_done + 2;     // [2] a slot's accumulators read (first CTA)
+  uint64_t *s_full = q_empty + 1;    // [slot][2] S written, and every product issued before it done
+  uint64_t *p_full = s_full + 4;     // [slot][2] P written (first CTA)
+  uint64_t *o_free = p_full + 4;     // [2] a slot's accumulators read (first CTA)
   uint64_t *mma_done = o_free + 2;   // every MMA issued has completed
-  static_assert(5 * NS + 11 == Lay::kBars, "mbarrier slots");
+  static_assert(5 * NS + 13 == Lay::kBars, "mbarrier slots");
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + Lay::off_tmem);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + Lay::off_abort);
   float2 *sm_ml = reinterpret_cast<float2 *>(smem + Lay::off_ml);
@@ -355,20 +362,20 @@ __global__ void __launch_bounds__(kPThreads, 1)
   if (threadIdx.x == 0) {
     for (int i = 0; i < NS; ++i) {
       mbar_init(&k_full[i], 1);
-      mbar_init(&k_empty[i], 1);
+      mbar_init(&k_empty[i], 2);
       mbar_init(&v_land[i], 1);
       mbar_init(&v_full[i], 8);
-      mbar_init(&v_empty[i], 1);
+      mbar_init(&v_empty[i], 2);
     }
     mbar_init(q_full, p.q_tma ? 1 : 8);
-    mbar_init(q_empty, 1);
-    for (int w = 0; w < 2; ++w) {
-      mbar_init(&s_full[w], 1);
-      mbar_init(&p_full[w], 8);
-      mbar_init(&o_done[w], 1);
-      mbar_init(&o_free[w], 8);
+    mbar_init(q_empty, 2);
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(&s_full[i], 1);
+      mbar_init(&p_full[i], 8);
     }
-    mbar_init(mma_done, 1);
+    mbar_init(&o_free[0], 8);
+    mbar_init(&o_free[1], 8);
+    mbar_init(mma_done, 2);
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -398,63 +405,68 @@ __global__ void __launch_bounds__(kPThreads, 1)
 
   if (warp >= 12) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
-    if (warp == 12 && rank == 0) {
+    if (warp < 14 && rank == 0) {
       // ------------------------------------------------------------------ MMA issue
-      // The whole warp walks the steps and an elected lane issues (in a branch that the
-      // compiler takes for divergent, an MMA costs about 100 clocks to issue).  One warp
-      // for both slots keeps them half a step apart: two, one a slot, let their MMAs
-      // interleave, so that both slots wait for the sum (456 -> 506 us at 128 x 5 rows x 32k).
-      constexpr uint32_t kIdescS = umma_idesc_bf16(2 * kPRows, kPKeys);
-      constexpr uint32_t kIdescO = umma_idesc_f16_bt(2 * kPRows, D);
-      const uint64_t q_base = umma_desc(smem_addr(smem + Lay::off_q)), k_base = umma_desc(smem_addr(smem + Lay::off_k)),
-                     v_base = umma_desc_v<D>(smem_addr(smem + Lay::off_v));
-      Ring<NS> kr;
-      Ring<NS> vr;
-      uint32_t ppar = 0, segs = 0;
+      const int w = warp - 12;
+      MmaState st;
+      st.q_desc = umma_desc(smem_addr(smem + Lay::off_q));
+      st.k_desc = umma_desc(smem_addr(smem + Lay::off_k));
+      st.v_desc = umma_desc_v<D>(smem_addr(smem + Lay::off_v));
+      st.s_tmem = tmem + w * 128;
+      st.o_tmem = tmem + 256 + w * D;
+      Ring<NS> kr, vr;
+      uint32_t ppar = 0, segs = 0;  // ppar: parity of the next pair of P
       bool ok = true;
       while (x < x1 && ok) {
         const PSeg sg = next_seg(p.g, line, x, x1);
+        // with two key tiles a step, slot 1 uses the second: one ahead in the rings
+        if (!sg.dual && w == 1) {
+          kr.advance();
+          vr.advance();
+        }
         ok = all_wait(q_full, segs & 1u, hdr, abort_flag);
-        // step s: O (+)= P V of step s - 1, then S = Q K^T of step s over the place of P
+        // step s: for either group of 64 keys, O (+)= P V of step s - 1, then S = Q K^T of step s over the
+        // place of that P.  The turn past the last step tells the softmax warps that all products are done.
         for (int s = 0; s <= sg.n && ok; ++s) {
-          for (int w = 0; w < 2 && ok; ++w) {
-            const bool opens = w == 0 || !sg.dual, closes = w == 1 || !sg.dual;  // a tile's first and last use
-            if (opens && !(ok = (s == sg.n || all_wait(&k_full[kr.stage], kr.parity, hdr, abort_flag)) &&
-                                (s == 0 || all_wait(&v_full[vr.stage], vr.parity, hdr, abort_flag))))
-              break;
-            if (s == 1 && segs > 0 && !(ok = all_wait(&o_free[w], (segs - 1) & 1u, hdr, abort_flag))) break;
-            if (s > 0 && !(ok = all_wait(&p_full[w], ppar, hdr, abort_flag))) break;
+          ok = (s == sg.n || all_wait(&k_full[kr.stage], kr.parity, hdr, abort_flag)) &&
+               (s == 0 || all_wait(&v_full[vr.stage], vr.parity, hdr, abort_flag)) &&
+               (s != 1 || segs == 0 || all_wait(&o_free[w], (segs - 1) & 1u, hdr, abort_flag));
+          const uint64_t kd = st.k_desc + static_cast<uint64_t>(kr.stage * (Lay::kKTile >> 4));
+          const uint64_t vd = st.v_desc + static_cast<uint64_t>(vr.stage * (Lay::kVTile >> 4));
+          const uint64_t qd = st.q_desc + static_cast<uint64_t>((sg.dual ? w : 0) * (Lay::kQTile >> 4));
+#pragma unroll
+          for (int sub = 0; sub < 2; ++sub) {
+            if (!ok || (s > 0 && !(ok = all_wait(&p_full[2 * w + sub], ppar, hdr, abort_flag)))) break;
             tc_fence_after();
-            const uint64_t vd = v_base + static_cast<uint64_t>(vr.stage * (Lay::kVTile >> 4));
-            const uint64_t kd = k_base + static_cast<uint64_t>(kr.stage * (Lay::kKTile >> 4));
-            const uint64_t qd = q_base + static_cast<uint64_t>((sg.dual ? w : 0) * (Lay::kQTile >> 4));
-            const uint32_t s_tmem = tmem + w * 128, o_tmem = tmem + 256 + w * D;
             if (elect_one()) {
               if (s > 0) {
-#pragma unroll
-                for (int kk = 0; kk < kPKeys / 16; ++kk)
-                  umma2_ts(o_tmem, s_tmem + kk * 8, vd + kk * (16 * D >> 4), kIdescO, (s > 1 || kk > 0) ? 1u : 0u);
-                if (closes) umma2_commit(&v_empty[vr.stage]);
+                product_pv<D>(st, vd, sub, s > 1 || sub > 0);
+                if (sub == 1) {  // a tile is freed by both slots; one that only this slot uses, by it alone
+                  umma2_commit(&v_empty[vr.stage]);
+                  if (!sg.dual) umma2_commit(&v_empty[vr.stage]);
+                }
               }
               if (s < sg.n) {
-#pragma unroll
-                for (int kk = 0; kk < D / 16; ++kk) {
-                  const uint64_t in_row = ((kk & 3) * 32) >> 4;
-                  umma2_ss(s_tmem, qd + (((kk >> 2) * Lay::kHalf) >> 4) + in_row,
-                           kd + (((kk >> 2) * Lay::kKHalf) >> 4) + in_row, kIdescS, kk > 0 ? 1u : 0u);
+                product_qk<D>(st, qd, kd, sub);
+                if (sub == 1) {
+                  umma2_commit(&k_empty[kr.stage]);
+                  if (!sg.dual) umma2_commit(&k_empty[kr.stage]);
+                  if (s == sg.n - 1) umma2_commit(q_empty);
                 }
-                umma2_commit(&s_full[w]);
-                if (closes) umma2_commit(&k_empty[kr.stage]);
-                if (s == sg.n - 1 && w == 1) umma2_commit(q_empty);
-              } else {
-                umma2_commit(&o_done[w]);
               }
+              umma2_commit(&s_full[2 * w + sub]);
             }
             __syncwarp();
-            if (closes && s > 0) vr.advance();
-            if (closes && s < sg.n) kr.advance();
           }
-          if (s > 0) ppar ^= 1u;
+          if (s > 0) {
+            vr.advance(sg.dual ? 1 : 2);
+            ppar ^= 1u;
+          }
+          if (s < sg.n) kr.advance(sg.dual ? 1 : 2);
+        }
+        if (!sg.dual && w == 1) {  // back to the tile after the segment's last
+          kr.retreat();
+          vr.retreat();
         }
         ++segs;
         x += sg.n;
@@ -462,7 +474,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
       if (elect_one()) umma2_commit(mma_done);
       __syncwarp();
       mbar_wait(mma_done, 0);
-    } else if (warp == 13 && lane == 0) {
+    } else if (warp == 14 && lane == 0) {
       // ------------------------------------------------------------------ K tiles
       tma_prefetch_desc(&kmap);
       tma_prefetch_desc(&vmap);
@@ -488,9 +500,11 @@ __global__ void __launch_bounds__(kPThreads, 1)
           if (!(ok = wait_or_abort(&k_empty[r.stage], r.parity ^ 1u, hdr, abort_flag))) break;
           if (rank == 0) mbar_arrive_expect_tx(&k_full[r.stage], 2 * Lay::kKTile);
           const uint32_t bar = in_first_cta(&k_full[r.stage]);
-          for (int hf = 0; hf < D / 64; ++hf)
-            tma2_load_4d(smem + Lay::off_k + r.stage * Lay::kKTile + hf * Lay::kKHalf, &kmap, bar, 64 * hf,
-                         key0 + rank * 64, sg.h, 0);
+          for (int b = 0; b < 2 * (D / 64); ++b) {
+            const int sub = b / (D / 64), hf = b % (D / 64);
+            tma2_load_4d(smem + Lay::off_k + r.stage * Lay::kKTile + sub * Lay::kKSub + hf * Lay::kKHalf, &kmap, bar,
+                         64 * hf, key0 + sub * 64 + rank * 32, sg.h, 0);
+          }
           ++n;  // counts a tile whose K is issued
           if (!(ok = wait_or_abort(&v_empty[r.stage], r.parity ^ 1u, hdr, abort_flag))) break;
           mbar_arrive_expect_tx(&v_land[r.stage], Lay::kVTile);
@@ -590,27 +604,39 @@ __global__ void __launch_bounds__(kPThreads, 1)
     const int tl = qd * 32 + lane;
     const uint32_t lane_off = static_cast<uint32_t>(qd * 32) << 16;
     const uint32_t s_addr = tmem + lane_off + w * 128, o_addr = tmem + lane_off + 256 + w * D;
-    uint32_t sc = 0, segs = 0;
+    uint32_t spar = 0;  // parity of the next pair of S
     while (x < x1) {
       const PSeg sg = next_seg(p.g, line, x, x1);
+      const int n = 2 * sg.n;
       float m = -INFINITY, l = 0.f;  // m: what P and O are scaled by (in units of log2)
-      for (int s = 0; s < sg.n; ++s) {
-        // tensor memory accesses are warp-collective: a warp skips a tile only as a whole
-        if (!all_wait(&s_full[w], sc++ & 1u, hdr, abort_flag)) continue;
-        tc_fence_after();
-        const int tile = sg.dual ? sg.first + s : 2 * (sg.first + s) + w;
-        const int nk = plen - tile * kPKeys;  // keys of this tile; zero or less: none
-        if (nk >= kPKeys)
-          softmax_tile<D, false>(s_addr, o_addr, p.sl2, nk, s == 0, m, l);
-        else
-          softmax_tile<D, true>(s_addr, o_addr, p.sl2, nk, s == 0, m, l);
-        tmem_wait_st();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) arrive_first_cta(&p_full[w]);
+      for (int i = 0; i < n; ++i) {
+        const int sub = i & 1;
+        // tensor memory accesses are warp-collective: a warp skips a group only as a whole
+        if (all_wait(&s_full[2 * w + sub], spar, hdr, abort_flag)) {
+          tc_fence_after();
+          const int tile = sg.dual ? sg.first + (i >> 1) : 2 * (sg.first + (i >> 1)) + w;
+          const int nk = plen - tile * kPKeys - sub * 64;  // keys of this group; zero or less: none
+          // the next S written means that every product before it, up to the group before this one, is done
+          auto settle = [&] {
+            const bool done = all_wait(&s_full[2 * w + (sub ^ 1)], sub ? spar ^ 1u : spar, hdr, abort_flag);
+            tc_fence_after();
+            return done;
+          };
+          if (nk >= 64)
+            softmax_group<D, false>(s_addr + sub * 64, o_addr, p.sl2, nk, i == 0, m, l, settle);
+          else
+            softmax_group<D, true>(s_addr + sub * 64, o_addr, p.sl2, nk, i == 0, m, l, settle);
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) arrive_first_cta(&p_full[2 * w + sub]);
+        }
+        if (sub) spar ^= 1u;
       }
-      // ---- end of the segment: this CTA's partial result of the pair
-      const bool got = all_wait(&o_done[w], segs & 1u, hdr, abort_flag);
+      // ---- end of the segment (every product done): this CTA's partial result of the pair
+      const bool even = all_wait(&s_full[2 * w], spar, hdr, abort_flag);
+      const bool got = all_wait(&s_full[2 * w + 1], spar, hdr, abort_flag) && even;
+      spar ^= 1u;
       tc_fence_after();
       if (!sg.dual) {  // both slots hold the same rows: slot 0 joins slot 1's result to its own
         if (w == 1) sm_ml[tl] = make_float2(m, l);
@@ -661,7 +687,6 @@ __global__ void __launch_bounds__(kPThreads, 1)
           if (!sg.dual) arrive_first_cta(&o_free[1]);
         }
       }
-      ++segs;
       x += sg.n;
     }
   }

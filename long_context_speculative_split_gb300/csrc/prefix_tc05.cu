@@ -30,6 +30,7 @@
 // 12 and 13 MMA issue for slot 0 / 1 (of the first CTA), 14 query rows, K and V tiles by TMA.  Registers a thread: 184, 88 and 56
 // for the three kinds of warp group (2 * 184 + 88 + 56 = 4 * 128, the launch's own total).
 #include <algorithm>
+#include <type_traits>
 
 #include "common.cuh"
 #include "prefix.cuh"
@@ -226,9 +227,10 @@ __device__ __forceinline__ uint32_t in_first_cta(const uint64_t *bar) {
   asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(a) : "r"(smem_addr(bar)));
   return a;
 }
-__device__ __forceinline__ void arrive_first_cta(const uint64_t *bar) {
-  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(in_first_cta(bar)) : "memory");
+__device__ __forceinline__ void arrive_cluster(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
+__device__ __forceinline__ void arrive_first_cta(const uint64_t *bar) { arrive_cluster(in_first_cta(bar)); }
 // A box of K into this CTA, its bytes counted by the barrier in the first CTA.
 __device__ __forceinline__ void tma2_load_4d(void *dst, const void *tmap, uint32_t bar, int c0, int c1, int c2, int c3) {
   asm volatile(
@@ -604,34 +606,41 @@ __global__ void __launch_bounds__(kPThreads, 1)
     const int tl = qd * 32 + lane;
     const uint32_t lane_off = static_cast<uint32_t>(qd * 32) << 16;
     const uint32_t s_addr = tmem + lane_off + w * 128, o_addr = tmem + lane_off + 256 + w * D;
-    uint32_t spar = 0;  // parity of the next pair of S
+    uint32_t spar = 0;          // parity of the next pair of S
+    float m = -INFINITY, l = 0.f;  // m: what P and O are scaled by (in units of log2)
+    const uint32_t p_bar[2] = {in_first_cta(&p_full[2 * w]), in_first_cta(&p_full[2 * w + 1])};
+    // the two groups of a tile
+    auto tile_of = [&](auto mask, int t, int left) {
+      constexpr bool kMask = decltype(mask)::value;
+#pragma unroll
+      for (int sub = 0; sub < 2; ++sub) {
+        // tensor memory accesses are warp-collective: a warp skips a group only as a whole
+        if (!all_wait(&s_full[2 * w + sub], spar, hdr, abort_flag)) continue;
+        tc_fence_after();
+        // the next S written means that every product before it, up to the group before this one, is done
+        auto settle = [&] {
+          const bool done = all_wait(&s_full[2 * w + (sub ^ 1)], sub ? spar ^ 1u : spar, hdr, abort_flag);
+          tc_fence_after();
+          return done;
+        };
+        softmax_group<D, kMask>(s_addr + sub * 64, o_addr, p.sl2, left - 64 * sub, t == 0 && sub == 0, m, l, settle);
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) arrive_cluster(p_bar[sub]);
+      }
+    };
     while (x < x1) {
       const PSeg sg = next_seg(p.g, line, x, x1);
-      const int n = 2 * sg.n;
-      float m = -INFINITY, l = 0.f;  // m: what P and O are scaled by (in units of log2)
-      for (int i = 0; i < n; ++i) {
-        const int sub = i & 1;
-        // tensor memory accesses are warp-collective: a warp skips a group only as a whole
-        if (all_wait(&s_full[2 * w + sub], spar, hdr, abort_flag)) {
-          tc_fence_after();
-          const int tile = sg.dual ? sg.first + (i >> 1) : 2 * (sg.first + (i >> 1)) + w;
-          const int nk = plen - tile * kPKeys - sub * 64;  // keys of this group; zero or less: none
-          // the next S written means that every product before it, up to the group before this one, is done
-          auto settle = [&] {
-            const bool done = all_wait(&s_full[2 * w + (sub ^ 1)], sub ? spar ^ 1u : spar, hdr, abort_flag);
-            tc_fence_after();
-            return done;
-          };
-          if (nk >= 64)
-            softmax_group<D, false>(s_addr + sub * 64, o_addr, p.sl2, nk, i == 0, m, l, settle);
-          else
-            softmax_group<D, true>(s_addr + sub * 64, o_addr, p.sl2, nk, i == 0, m, l, settle);
-          tmem_wait_st();
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) arrive_first_cta(&p_full[2 * w + sub]);
-        }
-        if (sub) spar ^= 1u;
+      m = -INFINITY;
+      l = 0.f;
+      for (int t = 0; t < sg.n; ++t, spar ^= 1u) {
+        const int tile = sg.dual ? sg.first + t : 2 * (sg.first + t) + w;
+        const int left = plen - tile * kPKeys;  // keys of this tile; zero or less: none
+        if (left >= kPKeys)
+          tile_of(std::false_type{}, t, left);
+        else
+          tile_of(std::true_type{}, t, left);
       }
       // ---- end of the segment (every product done): this CTA's partial result of the pair
       const bool even = all_wait(&s_full[2 * w], spar, hdr, abort_flag);

@@ -530,35 +530,45 @@ mgd_status mgd_prefix_attn(const void *q, const void *k_prefix, const void *v_pr
   a.ws = ws;
   a.stream = static_cast<cudaStream_t>(stream);
   unsigned char *w = static_cast<unsigned char *>(ws);
-  auto own = [&] {
-    return run_attention(q, k, v, kv_len, B, T, Hq, Hkv, D, kv_cap, kv_batch_stride, kv_head_stride, sm_scale, in_dtype,
-                         w + plan.off_own_o, MGD_F32, reinterpret_cast<float *>(w + plan.off_own_l), ws, ws_bytes,
-                         stream);
-  };
-  // The float32 attention clears the header ahead of its launch, so the prefix kernel raises its
-  // bits after it; the bf16 one closes the call's error word, so there the prefix goes first.
-  cudaError_t e;
   if (in_f32) {
-    if ((s = own()) != MGD_OK) return s;
-    e = launch_prefix_simt(plan, a);
-  } else {
-    // each CTA of a pair loads half of a key tile's keys of K and half of its columns of V
-    CUtensorMap km, vm;
-    if (encode_kv_tensor_map(&km, k_prefix, 1, Hkv, prefix_cap, D, prefix_head_stride * Hkv, prefix_head_stride, 32) != 0 ||
-        encode_kv_tensor_map(&vm, v_prefix, 1, Hkv, prefix_cap, D, prefix_head_stride * Hkv, prefix_head_stride, 128,
-                             D / 2) != 0)
-      return fail(MGD_ERR_CUDA, "cuTensorMapEncodeTiled failed");
-    CUtensorMap qm;
-    const int G = Hq / Hkv;
-    const bool q_tma = 128 % G == 0 && sm_scale >= 0.f &&
-                       encode_qwin_tensor_map(&qm, q, 1, B * T, Hq, D, G, 128 / G) == 0;
-    plan.grid = prefix_tc05_clusters(D, plan.grid);
-    e = launch_prefix_tc05(plan, a, km, vm, q_tma ? &qm : nullptr);
-    if (e == cudaSuccess && (s = own()) != MGD_OK) return s;
+    // this attention clears the header ahead of its launch, so the prefix kernel raises its bits after it
+    s = run_attention(q, k, v, kv_len, B, T, Hq, Hkv, D, kv_cap, kv_batch_stride, kv_head_stride, sm_scale, in_dtype,
+                      w + plan.off_own_o, MGD_F32, reinterpret_cast<float *>(w + plan.off_own_l), ws, ws_bytes, stream);
+    if (s != MGD_OK) return s;
+    cudaError_t e = launch_prefix_simt(plan, a);
+    if (e == cudaSuccess) e = launch_prefix_merge(plan, a);
+    return e == cudaSuccess ? ok() : cuda_fail(e, "prefix attention (float32) launch");
   }
-  if (e != cudaSuccess) return cuda_fail(e, "prefix attention launch");
-  e = launch_prefix_merge(plan, a);
-  return e == cudaSuccess ? ok() : cuda_fail(e, "prefix merge launch");
+  AttnArgs o;
+  o.q = q;
+  o.k = k;
+  o.v = v;
+  o.kv_len = kv_len;
+  o.kv_batch_stride = kv_batch_stride;
+  o.kv_head_stride = kv_head_stride;
+  o.sm_scale = sm_scale;
+  o.out = w + plan.off_own_o;
+  o.out_bf16 = 0;
+  o.lse = reinterpret_cast<float *>(w + plan.off_own_l);
+  o.ws = ws;
+  o.stream = a.stream;
+  // each CTA of a pair loads half of a key group's keys of K and half of a key tile's columns of V
+  const int64_t all = prefix_head_stride * Hkv;
+  const int G = Hq / Hkv;
+  CUtensorMap pk, pv, pq, km, vm;
+  if (encode_kv_tensor_map(&pk, k_prefix, 1, Hkv, prefix_cap, D, all, prefix_head_stride, 32) != 0 ||
+      encode_kv_tensor_map(&pv, v_prefix, 1, Hkv, prefix_cap, D, all, prefix_head_stride, 128, D / 2) != 0 ||
+      encode_kv_tensor_map(&km, k, B, Hkv, kv_cap, D, kv_batch_stride, kv_head_stride) != 0 ||
+      encode_kv_tensor_map(&vm, v, B, Hkv, kv_cap, D, kv_batch_stride, kv_head_stride) != 0)
+    return fail(MGD_ERR_CUDA, "cuTensorMapEncodeTiled failed");
+  const bool q_tma =
+      128 % G == 0 && sm_scale >= 0.f && encode_qwin_tensor_map(&pq, q, 1, B * T, Hq, D, G, 128 / G) == 0;
+  plan.grid = prefix_share(plan, prefix_tc05_clusters(D, plan.grid), current_sm_count());
+  cudaError_t e = clear_attention_tickets(plan.own, ws, a.stream);
+  if (e == cudaSuccess) e = launch_prefix_tc05(plan, a, pk, pv, q_tma ? &pq : nullptr);
+  if (e == cudaSuccess) e = launch_attention_beside(plan.own, o, km, vm);
+  if (e == cudaSuccess) e = launch_prefix_merge(plan, a);
+  return e == cudaSuccess ? ok() : cuda_fail(e, "prefix attention launch");
 }
 
 mgd_status mgd_rope_frequencies(int rotary_dim, double base, int scaling, const double *params, uint64_t *turns,

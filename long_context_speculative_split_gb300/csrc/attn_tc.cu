@@ -31,7 +31,9 @@
 //   * at the end of a unit the 4 warps merge in shared memory; a unit that
 //     covers the whole sequence writes the final output, otherwise it writes
 //     a partial (O, lse) and the CTA that completes the last chunk of that
-//     sequence merges all partials (atomic ticket, no waiting).
+//     sequence merges all partials (atomic ticket, no waiting);
+//   * behind a shared prefix (kBeside) the kernel runs beside the prefix kernel, on the
+//     SMs that it leaves free, and only waits for it before it ends.
 #include <algorithm>
 
 #include "common.cuh"
@@ -87,13 +89,13 @@ struct Layout {
   static constexpr int alloc = bytes + 1024;  // slack to align the base to 1024
 };
 
-template <int D, int NT, int MINB>
+template <int D, int NT, int MINB, bool kBeside>
 __global__ void __launch_bounds__(kThreads, MINB)
     attn_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                    const __nv_bfloat16 *__restrict__ q, const int32_t *__restrict__ kv_len,
                    float *__restrict__ out_f32, __nv_bfloat16 *__restrict__ out_bf16, float *__restrict__ lse_out,
                    unsigned char *__restrict__ ws, KParams p) {
-  pdl_launch_dependents();
+  if constexpr (!kBeside) pdl_launch_dependents();
   using Lay = Layout<D, NT>;
   extern __shared__ unsigned char smem_raw[];
   unsigned char *smem = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -133,14 +135,17 @@ __global__ void __launch_bounds__(kThreads, MINB)
     const int u = static_cast<int>(blockIdx.x);
     const int bh = (u / p.nchunk) / p.RG;
     const int row0 = (u % p.nchunk) * p.C;
-    for (int t = 0; t < 2; ++t)
+    for (int t = 0; t < (kBeside ? 0 : 2); ++t)
       for (int h = 0; h < Lay::kBoxes; ++h) {
         tma_prefetch_l2_4d(&kmap, h * 64, row0 + t * kTileKeys, bh % p.Hkv, bh / p.Hkv);
         tma_prefetch_l2_4d(&vmap, h * 64, row0 + t * kTileKeys, bh % p.Hkv, bh / p.Hkv);
       }
   }
   __syncthreads();
-  pdl_wait();  // set-up above changes no global memory; everything below comes after the previous kernel
+  // Set-up above changes no global memory; everything below comes after the previous kernel.  Beside the
+  // prefix kernel it comes after whatever was before that one: the prefix kernel lets this one start
+  // after its own wait, and the two share no memory that either writes.
+  if constexpr (!kBeside) pdl_wait();
 
   // ====================================================================== producer
   if (warp == kConsumerWarps) {
@@ -148,12 +153,14 @@ __global__ void __launch_bounds__(kThreads, MINB)
     int stage = 0;
     uint32_t phase = 0;
     bool ok = true;
-    bool first = true;
+    bool first = !kBeside;
     unsigned claims = 0;  // successful claims from the counter
+    // every CTA's first unit is its own index (no counter round trip before the first
+    // load); later units come from the counter.  Beside the prefix kernel all of them do:
+    // the CTAs that find an SM at once take what the others would start later with.
+    const unsigned firsts = kBeside ? 0u : gridDim.x;
     while (ok) {
-      // every CTA's first unit is its own index (no counter round trip before the first
-      // load); later units come from the counter
-      const unsigned u = first ? blockIdx.x : gridDim.x + atomicAdd(&hdr->next_unit, 1u);
+      const unsigned u = first ? blockIdx.x : firsts + atomicAdd(&hdr->next_unit, 1u);
       if (u >= p.total_units) break;
       claims += first ? 0u : 1u;
       first = false;
@@ -219,7 +226,11 @@ __global__ void __launch_bounds__(kThreads, MINB)
     // This CTA's claims are over: it checks in (its consumers need not: they claim nothing,
     // and their only error bits, timeouts, land in one of the two words either way).
     // From a ready header the counter hands out exactly the units past the first wave.
-    call_check_in(hdr, gridDim.x, blockIdx.x, claims, p.total_units - gridDim.x);
+    if constexpr (kBeside) {  // the next kernel waits for this one alone: it ends after the prefix kernel
+      pdl_wait();
+      pdl_launch_dependents();
+    }
+    call_check_in(hdr, gridDim.x, blockIdx.x, claims, p.total_units - firsts);
     return;
   }
 
@@ -620,10 +631,10 @@ __global__ void __launch_bounds__(kThreads, MINB)
   }
 }
 
-template <int D, int NT>
+template <int D, int NT, bool kBeside>
 cudaError_t launch_one(const AttnPlan &pl, const AttnArgs &a, const CUtensorMap &kmap, const CUtensorMap &vmap) {
   constexpr int MINB = (NT <= 3) ? 2 : 1;
-  auto kern = attn_tc_kernel<D, NT, MINB>;
+  auto kern = attn_tc_kernel<D, NT, MINB, kBeside>;
   const int smem = Layout<D, NT>::alloc;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
@@ -659,39 +670,50 @@ cudaError_t launch_one(const AttnPlan &pl, const AttnArgs &a, const CUtensorMap 
                     static_cast<unsigned char *>(a.ws), kp);
 }
 
-}  // namespace
-
-int attn_tc_min_blocks(int NT) { return NT <= 3 ? 2 : 1; }
-
-cudaError_t launch_attention_tc(const AttnPlan &pl, const AttnArgs &a, const CUtensorMap &kmap,
-                                const CUtensorMap &vmap) {
-  // The header needs no clearing launch: the kernel leaves it ready for the next call
-  // (the workspace is zero-filled before its first use).  The merge tickets of split
-  // sequences are cleared here, since a call of another shape may have written
-  // partial results where this call keeps them.
-  if (pl.nchunk > 1) {
-    cudaError_t e = cudaMemsetAsync(static_cast<unsigned char *>(a.ws) + pl.off_tickets, 0,
-                                    pl.off_part_o - pl.off_tickets, a.stream);
-    if (e != cudaSuccess) return e;
-  }
+template <bool kBeside>
+cudaError_t launch_any(const AttnPlan &pl, const AttnArgs &a, const CUtensorMap &kmap, const CUtensorMap &vmap) {
   if (pl.D == 128) {
     switch (pl.NT) {
-      case 1: return launch_one<128, 1>(pl, a, kmap, vmap);
-      case 2: return launch_one<128, 2>(pl, a, kmap, vmap);
-      case 3: return launch_one<128, 3>(pl, a, kmap, vmap);
-      default: return launch_one<128, 4>(pl, a, kmap, vmap);
+      case 1: return launch_one<128, 1, kBeside>(pl, a, kmap, vmap);
+      case 2: return launch_one<128, 2, kBeside>(pl, a, kmap, vmap);
+      case 3: return launch_one<128, 3, kBeside>(pl, a, kmap, vmap);
+      default: return launch_one<128, 4, kBeside>(pl, a, kmap, vmap);
     }
   } else {
     switch (pl.NT) {
-      case 1: return launch_one<64, 1>(pl, a, kmap, vmap);
-      case 2: return launch_one<64, 2>(pl, a, kmap, vmap);
-      case 3: return launch_one<64, 3>(pl, a, kmap, vmap);
-      default: return launch_one<64, 4>(pl, a, kmap, vmap);
+      case 1: return launch_one<64, 1, kBeside>(pl, a, kmap, vmap);
+      case 2: return launch_one<64, 2, kBeside>(pl, a, kmap, vmap);
+      case 3: return launch_one<64, 3, kBeside>(pl, a, kmap, vmap);
+      default: return launch_one<64, 4, kBeside>(pl, a, kmap, vmap);
     }
   }
 }
 
-AttnPlan plan_attention(int B, int T, int Hq, int Hkv, int D, int kv_cap, int sm_count) {
+}  // namespace
+
+int attn_tc_min_blocks(int NT) { return NT <= 3 ? 2 : 1; }
+
+// The header needs no clearing launch: the kernel leaves it ready for the next call
+// (the workspace is zero-filled before its first use).  The merge tickets of split
+// sequences are cleared here, since a call of another shape may have written
+// partial results where this call keeps them.
+cudaError_t clear_attention_tickets(const AttnPlan &pl, void *ws, cudaStream_t stream) {
+  if (pl.nchunk <= 1) return cudaSuccess;
+  return cudaMemsetAsync(static_cast<unsigned char *>(ws) + pl.off_tickets, 0, pl.off_part_o - pl.off_tickets, stream);
+}
+
+cudaError_t launch_attention_tc(const AttnPlan &pl, const AttnArgs &a, const CUtensorMap &kmap,
+                                const CUtensorMap &vmap) {
+  cudaError_t e = clear_attention_tickets(pl, a.ws, a.stream);
+  return e != cudaSuccess ? e : launch_any<false>(pl, a, kmap, vmap);
+}
+
+cudaError_t launch_attention_beside(const AttnPlan &pl, const AttnArgs &a, const CUtensorMap &kmap,
+                                    const CUtensorMap &vmap) {
+  return launch_any<true>(pl, a, kmap, vmap);
+}
+
+AttnPlan plan_attention(int B, int T, int Hq, int Hkv, int D, int kv_cap, int sm_count, bool whole) {
   AttnPlan p{};
   p.B = B;
   p.T = T;
@@ -717,7 +739,8 @@ AttnPlan plan_attention(int B, int T, int Hq, int Hkv, int D, int kv_cap, int sm
   // 16k keys 0.215 -> 0.172 ms and 0.373 -> 0.320 ms).
   int C = 16384;
   const int cmin = std::max(256, ((kv_cap + 63) / 64 + 63) / 64 * 64);
-  if (p.pairs > slots)
+  // `whole`: the same for any number of pairs (the own caches behind a shared prefix, which are short).
+  if (p.pairs > slots && !whole)
     while (C > cmin && static_cast<long long>(p.pairs) * ((kv_cap + C - 1) / C) < 3LL * slots) C /= 2;
   if (C < cmin) C = cmin;
   p.C = C;

@@ -74,7 +74,7 @@ struct AttnPlan {
   int grid;       // persistent CTAs
   size_t off_tickets, off_part_o, off_part_l, ws_bytes;
 };
-AttnPlan plan_attention(int B, int T, int Hq, int Hkv, int D, int kv_cap, int sm_count);
+AttnPlan plan_attention(int B, int T, int Hq, int Hkv, int D, int kv_cap, int sm_count, bool whole = false);
 
 struct AttnArgs {
   const void *q;
@@ -92,6 +92,7 @@ struct AttnArgs {
 // bf16 inputs, tensor cores, TMA tiles, persistent split-KV with in-kernel merge.
 cudaError_t launch_attention_tc(const AttnPlan &p, const AttnArgs &a, const CUtensorMap &kmap,
                                 const CUtensorMap &vmap);
+cudaError_t clear_attention_tickets(const AttnPlan &p, void *ws, cudaStream_t stream);
 // Any-dtype CUDA-core attention, one CTA per (sequence, KV head).
 size_t simt_attention_ws_bytes();
 cudaError_t launch_attention_simt(const AttnPlan &p, const AttnArgs &a);
@@ -125,6 +126,8 @@ struct PrefixPlan {
 };
 PrefixPlan plan_prefix(int B, int T, int Hq, int Hkv, int D, int prefix_cap, int kv_cap, int in_f32, int sm_count);
 
+int prefix_share(const PrefixPlan &p, int most, int sm_count);  // clusters of the bf16 prefix kernel
+
 struct PrefixArgs {
   const void *q;
   const void *k;  // [Hkv, prefix_cap, D]
@@ -144,6 +147,10 @@ cudaError_t launch_prefix_tc05(const PrefixPlan &p, const PrefixArgs &a, const C
                                const CUtensorMap &vmap, const CUtensorMap *qmap);  // bf16; qmap nullable
 cudaError_t launch_prefix_simt(const PrefixPlan &p, const PrefixArgs &a);                           // float32
 cudaError_t launch_prefix_merge(const PrefixPlan &p, const PrefixArgs &a);
+// The bf16 attention over the own caches, launched right after the prefix kernel: it runs beside that
+// one on the SMs that are left, and its results are complete when both are.
+cudaError_t launch_attention_beside(const AttnPlan &p, const AttnArgs &a, const CUtensorMap &kmap,
+                                    const CUtensorMap &vmap);
 
 // ------------------------------------------------------------------ SnapKV
 // Keys per job of the one-read tcgen05 scorer (12 tiles of 128 keys): small

@@ -5,8 +5,8 @@
 // With s_j = scale <q, k_j>, the softmax over prefix and own keys splits exactly:
 //   (O_P, l_P), (O_b, l_b) = the two parts' outputs and log-sum-exps
 //   l = log(e^{l_P} + e^{l_b}),  O = e^{l_P - l} O_P + e^{l_b - l} O_b.
-// The own part is the verify attention kernel with a float32 output; the prefix
-// part has B * T * G query rows a KV head instead of T * G, which turns the one
+// The own part is the verify attention kernel with a float32 output; the prefix part has
+// B * T * G query rows a KV head instead of T * G, which turns the one
 // read of the prefix into a matrix product.
 #include <algorithm>
 
@@ -179,61 +179,67 @@ __global__ void __launch_bounds__(kSThreads)
 }
 
 // ---------------------------------------------------------------- merge
-// One warp per query row: the own part and the row's partial results over the
-// prefix, weighted by their log-sum-exps.
-constexpr int kMergeWarps = 8;
+// D / 4 lanes per query row, four columns each: the own part and the row's partial results over the
+// prefix, weighted by their log-sum-exps.  Bound by L2: own part, partial results and output once each.
+constexpr int kMergeThreads = 256;
 
 template <int D>
-__global__ void __launch_bounds__(kMergeWarps * 32)
+__global__ void __launch_bounds__(kMergeThreads)
     prefix_merge_kernel(const float *__restrict__ own_o, const float *__restrict__ own_l,
                         const float *__restrict__ part_o, const float *__restrict__ part_l,
                         const int32_t *__restrict__ prefix_len, PrefixGeom g, int grid, float *__restrict__ out_f32,
                         __nv_bfloat16 *__restrict__ out_bf16, float *__restrict__ lse_out) {
   pdl_launch_dependents();
   pdl_wait();
-  constexpr int E = D / 32;  // floats of a row per lane
-  const int lane = threadIdx.x & 31;
-  const int64_t row = static_cast<int64_t>(blockIdx.x) * kMergeWarps + (threadIdx.x >> 5);  // (b, t, hq)
+  constexpr int kLanes = D / 4;
+  const int d = 4 * (threadIdx.x % kLanes);
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * (kMergeThreads / kLanes) + threadIdx.x / kLanes;  // (b, t, hq)
   if (row >= static_cast<int64_t>(g.B) * g.T * g.Hq) return;
   const int plen = prefix_len[0];
+  float m = own_l[row], sum = 1.f;
+  float4 o = *reinterpret_cast<const float4 *>(own_o + row * D + d);
   if (plen < 0 || plen > g.prefix_cap) return;  // flagged by the prefix kernel
-  const int hq = static_cast<int>(row % g.Hq), bt = static_cast<int>(row / g.Hq);
-  const int h = hq / g.G, r = bt * g.G + hq % g.G;
-  const int rt = r / g.tile_rows, lr = r % g.tile_rows;
-  float m = own_l[row], wsum = 1.f, o[E];
-  float buf[E];
-#pragma unroll
-  for (int e = 0; e < E; ++e) o[e] = own_o[row * D + lane * E + e];
   if (plen > 0) {
+    const int hq = static_cast<int>(row % g.Hq), bt = static_cast<int>(row / g.Hq);
+    const int h = hq / g.G, r = bt * g.G + hq % g.G;
+    const int rt = r / g.tile_rows, lr = r % g.tile_rows;
     const PrefixLine w = prefix_line(g, plen, grid);
     const int begin = prefix_pair_begin(w, h, rt);
     const int c0 = prefix_cta_of(w, begin), c1 = prefix_cta_of(w, begin + prefix_pair_steps(g, w, rt) - 1);
-    for (int c = c0; c <= c1; ++c) {
-      const int64_t at = static_cast<int64_t>(c + h * g.RT + rt) * g.slot_rows + lr;
-      const float ls = part_l[at];
+    const int64_t at0 = static_cast<int64_t>(h * g.RT + rt) * g.slot_rows + lr;
+    for (int c = c0; c <= c1; c += 4) {  // four partial results on their way at once
+      float l[4];
+      float4 x[4];
 #pragma unroll
-      for (int e = 0; e < E; ++e) buf[e] = part_o[at * D + lane * E + e];
-      const float mn = fmaxf(m, ls);
-      if (mn == -INFINITY) continue;  // neither part has a finite score
-      const float a = expf(m - mn), b = expf(ls - mn);
-      wsum = wsum * a + b;
+      for (int i = 0; i < 4; ++i) {
+        const int64_t at = at0 + static_cast<int64_t>(min(c + i, c1)) * g.slot_rows;
+        l[i] = __ldcg(part_l + at);
+        x[i] = __ldcg(reinterpret_cast<const float4 *>(part_o + at * D + d));
+      }
 #pragma unroll
-      for (int e = 0; e < E; ++e) o[e] = o[e] * a + buf[e] * b;
-      m = mn;
+      for (int i = 0; i < 4; ++i) {
+        const float mn = fmaxf(m, l[i]);
+        if (c + i > c1 || mn == -INFINITY) continue;  // past the last, or no finite score so far
+        const float a = expf(m - mn), b = expf(l[i] - mn);
+        sum = sum * a + b;
+        o.x = o.x * a + x[i].x * b;
+        o.y = o.y * a + x[i].y * b;
+        o.z = o.z * a + x[i].z * b;
+        o.w = o.w * a + x[i].w * b;
+        m = mn;
+      }
     }
   }
-  const float inv = 1.f / wsum;
-#pragma unroll
-  for (int e = 0; e < E; ++e) o[e] *= inv;
-  if (out_bf16) {
-#pragma unroll
-    for (int e = 0; e < E; e += 2)
-      *reinterpret_cast<uint32_t *>(out_bf16 + row * D + lane * E + e) = pack_bf16(o[e], o[e + 1]);
-  } else {
-#pragma unroll
-    for (int e = 0; e < E; ++e) out_f32[row * D + lane * E + e] = o[e];
-  }
-  if (lse_out && lane == 0) lse_out[row] = m + logf(wsum);
+  const float inv = 1.f / sum;
+  o.x *= inv;
+  o.y *= inv;
+  o.z *= inv;
+  o.w *= inv;
+  if (out_bf16)
+    *reinterpret_cast<uint2 *>(out_bf16 + row * D + d) = make_uint2(pack_bf16(o.x, o.y), pack_bf16(o.z, o.w));
+  else
+    *reinterpret_cast<float4 *>(out_f32 + row * D + d) = o;
+  if (lse_out && d == 0) lse_out[row] = m + logf(sum);
 }
 
 template <int D>
@@ -258,14 +264,37 @@ cudaError_t launch_prefix_simt(const PrefixPlan &p, const PrefixArgs &a) {
 cudaError_t launch_prefix_merge(const PrefixPlan &p, const PrefixArgs &a) {
   const unsigned char *ws = static_cast<const unsigned char *>(a.ws);
   const int64_t rows = static_cast<int64_t>(p.g.B) * p.g.T * p.g.Hq;
-  const dim3 grid(static_cast<unsigned>((rows + kMergeWarps - 1) / kMergeWarps));
-  return launch_pdl(p.g.D == 128 ? prefix_merge_kernel<128> : prefix_merge_kernel<64>, grid, dim3(kMergeWarps * 32), 0,
+  const int per = kMergeThreads / (p.g.D / 4);
+  const dim3 grid(static_cast<unsigned>((rows + per - 1) / per));
+  return launch_pdl(p.g.D == 128 ? prefix_merge_kernel<128> : prefix_merge_kernel<64>, grid, dim3(kMergeThreads), 0,
                     a.stream, reinterpret_cast<const float *>(ws + p.off_own_o),
                     reinterpret_cast<const float *>(ws + p.off_own_l),
                     reinterpret_cast<const float *>(ws + p.off_part_o),
                     reinterpret_cast<const float *>(ws + p.off_part_l), a.prefix_len, p.g, p.grid,
                     a.out_bf16 ? nullptr : static_cast<float *>(a.out),
                     a.out_bf16 ? static_cast<__nv_bfloat16 *>(a.out) : nullptr, a.lse);
+}
+
+// The prefix kernel is bound by its tensor cores and their latency, the attention over the own caches by
+// HBM, so the prefix kernel takes only part of the SMs and the other one runs beside it.  Its clusters
+// out of `most`: the number that by these measured rates ends both first -- 1.7 us a step, 100 GB/s of
+// own cache an SM, 6600 GB/s in all -- with the capacities in place of the lengths, which only the device
+// knows.
+int prefix_share(const PrefixPlan &p, int most, int sm_count) {
+  const PrefixLine line = prefix_line(p.g, p.g.prefix_cap, most);
+  const double own = 4.0 * p.g.B * p.g.Hkv * p.own_cap * p.g.D;  // bytes of K and V
+  double best = 0.0;
+  int share = most;
+  for (int n = most; n >= (most + 1) / 2; --n) {
+    const double prefix_us = 1.7 * ((line.total + n - 1) / n);
+    const double beside = 0.1e6 * (sm_count - 2 * n) * prefix_us;
+    const double us = prefix_us + (own > beside ? (own - beside) / 6.6e6 : 0.0);
+    if (n == most || us < best) {
+      best = us;
+      share = n;
+    }
+  }
+  return share;
 }
 
 PrefixPlan plan_prefix(int B, int T, int Hq, int Hkv, int D, int prefix_cap, int kv_cap, int in_f32, int sm_count) {
@@ -284,7 +313,7 @@ PrefixPlan plan_prefix(int B, int T, int Hq, int Hkv, int D, int prefix_cap, int
   g.RT = (g.R + g.tile_rows - 1) / g.tile_rows;
   g.last_half = !in_f32 && g.R - (g.RT - 1) * g.tile_rows <= 256;
   g.slot_rows = std::min(g.tile_rows, g.R);
-  p.own = plan_attention(B, T, Hq, Hkv, D, kv_cap, sm_count);
+  p.own = plan_attention(B, T, Hq, Hkv, D, kv_cap, sm_count, !in_f32);
   p.own_cap = kv_cap;
   // what fits at once: two CTAs of 116 KB shared memory an SM; clusters of two CTAs of 226 KB
   p.grid = in_f32 ? 2 * sm_count : std::max(1, sm_count / 2);

@@ -360,7 +360,6 @@ __global__ void __launch_bounds__(kPThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = static_cast<int>(cluster_rank());
 
-  pdl_launch_dependents();
   if (threadIdx.x == 0) {
     for (int i = 0; i < NS; ++i) {
       mbar_init(&k_full[i], 1);
@@ -393,6 +392,9 @@ __global__ void __launch_bounds__(kPThreads, 1)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   pdl_wait();
+  // The attention over the own caches may start on the SMs that are left: whatever came before this
+  // kernel is complete, and it waits for this one before it reads the partial results.
+  pdl_launch_dependents();
 
   const int plen = prefix_len[0];
   const bool valid = plen >= 0 && plen <= p.g.prefix_cap;

@@ -512,7 +512,7 @@ mgd_status mgd_rope_append(const void *q, int64_t q_token_stride, const void *k_
  * that holds a NaN or +inf, or nothing but -inf, has no distribution: logprob
  * and entropy NaN, rank -1, no alternatives.  Sums in float32.  A token outside
  * [-1, V) is treated as -1 and flagged (MGD_DEVERR_TOKEN).
- * Supported: 1 <= V < 2^31; 0 <= K <= 32; row_stride >= V; any alignment of
+ * Supported: 1 <= V <= 2^30; 0 <= K <= 32; row_stride >= V; any alignment of
  * the element type.
  * ------------------------------------------------------------------------ */
 size_t mgd_logprobs_workspace_size(int R, int V, int K);

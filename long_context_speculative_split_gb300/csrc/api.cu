@@ -709,6 +709,7 @@ mgd_status mgd_token_logprobs(const void *logits, int64_t row_stride, mgd_dtype 
   const NvtxRange nvtx_range("mgd_token_logprobs");
   if (R < 0) return fail(MGD_ERR_INVALID_ARG, "R must be >= 0 (got %d)", R);
   if (V < 1) return fail(MGD_ERR_INVALID_ARG, "V must be >= 1 (got %d)", V);
+  if (V > (1 << 30)) return fail(MGD_ERR_UNSUPPORTED, "V must be at most 2^30 (got %d)", V);
   if (K < 0 || K > 32) return fail(MGD_ERR_UNSUPPORTED, "K must be in [0, 32] (got %d)", K);
   if (dtype != MGD_BF16 && dtype != MGD_F32) return fail(MGD_ERR_INVALID_ARG, "bad dtype %d", dtype);
   if (row_stride < V) return fail(MGD_ERR_INVALID_ARG, "row_stride %lld < V %d", static_cast<long long>(row_stride), V);

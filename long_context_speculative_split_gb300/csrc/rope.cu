@@ -10,16 +10,22 @@
 // radians.  The cosine and sine of each (row, pair) are computed once in float32
 // and shared by all heads; rotated values are rounded once, to the data's type.
 //
-// Bound by HBM: every element is read once and written once.
+// Bound by HBM: every element is read once and written once.  A CTA takes one new
+// row: its threads first ask for their elements (16 bytes a load, all of a row's
+// loads in flight at once for up to kBatch a thread), then compute the angles, then
+// turn and store.  Threads are laid out as (chunk of a head, head), so a thread's
+// place in its heads, its angles with it, is the same for all heads it handles.
 #include "common.cuh"
 
 namespace mgd {
 namespace {
 
-constexpr int kRopeThreads = 256;
+constexpr int kBatch = 4;  // items a thread has in flight
 
 struct RopeParams {
   int T, Hq, Hkv, D, half, interleaved, kv_cap, pos_stride;
+  int items;      // work items of a head: pairs of 16-byte chunks that turn together, then chunks that pass
+  int pair_items; // of which turn
   int64_t q_stride, k_stride, v_stride;  // elements between the rows of two tokens
   int64_t kv_bstride, kv_hstride;
   float magnitude;
@@ -32,8 +38,31 @@ __device__ __forceinline__ float from_f32<float>(float x) { return x; }
 template <>
 __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float x) { return __float2bfloat16_rn(x); }
 
-template <typename Tin>
-__global__ void __launch_bounds__(kRopeThreads)
+// 16 bytes of a row, or one element where the rotated part does not split into whole chunks.
+template <typename Tin, int VE>
+struct Chunk {
+  Tin v[VE];
+};
+template <typename Tin, int VE>
+__device__ __forceinline__ Chunk<Tin, VE> load_chunk(const Tin *p) {
+  Chunk<Tin, VE> c;
+  if constexpr (VE == 1)
+    c.v[0] = *p;
+  else
+    *reinterpret_cast<uint4 *>(c.v) = __ldcs(reinterpret_cast<const uint4 *>(p));
+  return c;
+}
+template <typename Tin, int VE>
+__device__ __forceinline__ void store_chunk(Tin *p, const Chunk<Tin, VE> &c) {
+  if constexpr (VE == 1)
+    *p = c.v[0];
+  else
+    *reinterpret_cast<uint4 *>(p) = *reinterpret_cast<const uint4 *>(c.v);
+}
+
+// VE: elements of a chunk (16 bytes, or 1).  blockDim = (items rounded to a power of two, heads at once).
+template <typename Tin, int VE, bool kInter>
+__global__ void __launch_bounds__(512)
     rope_append_kernel(const Tin *__restrict__ q, const Tin *__restrict__ kn, const Tin *__restrict__ vn,
                        const unsigned long long *__restrict__ turns, const int32_t *__restrict__ kv_len,
                        const int32_t *__restrict__ new_len, const int32_t *__restrict__ pos_offset,
@@ -42,73 +71,119 @@ __global__ void __launch_bounds__(kRopeThreads)
   pdl_launch_dependents();
   pdl_wait();
   extern __shared__ float2 cs[];  // [half]
+  const int tid = threadIdx.y * blockDim.x + threadIdx.x, nthreads = blockDim.x * blockDim.y;
   if (blockIdx.x == 0) {
     // one CTA looks at every sequence and writes the call's error bits
     int bad = 0;
-    for (int i = threadIdx.x; i < B; i += kRopeThreads) {
+    for (int i = tid; i < B; i += nthreads) {
       const int L = kv_len[i], n = new_len ? new_len[i] : p.T;
       bad |= n < 0 || n > p.T || L < n || L > p.kv_cap;
     }
     bad = __syncthreads_or(bad);
-    if (threadIdx.x == 0) {
+    if (tid == 0) {
       hdr->err[0] = bad ? 0x1u : 0u;
       hdr->err[1] = 0u;
     }
   }
   const int64_t token = blockIdx.x;
-  const int b = static_cast<int>(token / p.T), t = static_cast<int>(token % p.T);
+  const int b = static_cast<int>(blockIdx.x / static_cast<unsigned>(p.T)), t = static_cast<int>(token - static_cast<int64_t>(b) * p.T);
   const int L = kv_len[b], n = new_len ? new_len[b] : p.T;
+  const int off = pos_offset ? pos_offset[b * p.pos_stride] : 0;
   if (n < 0 || n > p.T || L < n || L > p.kv_cap || t >= n) return;
   const int row = L - n + t;
-  const int64_t pos = static_cast<int64_t>(row) + (pos_offset ? pos_offset[b * p.pos_stride] : 0);
-  for (int i = threadIdx.x; i < p.half; i += kRopeThreads) {
-    const long long a = static_cast<long long>(static_cast<unsigned long long>(pos) * turns[i]);
-    float sn, cn;
-    sincospif(static_cast<float>(a) * 0x1p-63f, &sn, &cn);
-    cs[i] = make_float2(cn * p.magnitude, sn * p.magnitude);
-  }
-  __syncthreads();
+  const int64_t pos = static_cast<int64_t>(row) + off;
   const int heads = p.Hq + 2 * p.Hkv;
-  const int units = p.half + (p.D - 2 * p.half);  // pairs, then the elements past the rotated part
-  for (int i = threadIdx.x; i < heads * units; i += kRopeThreads) {
-    const int h = i / units, u = i % units;
-    const Tin *src;
-    Tin *dst;
-    bool turn = true;
-    if (h < p.Hq) {
-      src = q + token * p.q_stride + static_cast<int64_t>(h) * p.D;
-      dst = q_out + (token * p.Hq + h) * p.D;
-    } else if (h < p.Hq + p.Hkv) {
-      const int hk = h - p.Hq;
-      src = kn + token * p.k_stride + static_cast<int64_t>(hk) * p.D;
-      dst = k + b * p.kv_bstride + hk * p.kv_hstride + static_cast<int64_t>(row) * p.D;
-    } else {
-      const int hk = h - p.Hq - p.Hkv;
-      src = vn + token * p.v_stride + static_cast<int64_t>(hk) * p.D;
-      dst = v + b * p.kv_bstride + hk * p.kv_hstride + static_cast<int64_t>(row) * p.D;
-      turn = false;
+  const int64_t cache = b * p.kv_bstride + static_cast<int64_t>(row) * p.D;
+  const Tin *qs = q + token * p.q_stride, *ks = kn + token * p.k_stride, *vs = vn + token * p.v_stride;
+  Tin *qd = q_out + token * p.Hq * p.D;
+  auto source = [&](int h) {
+    return h < p.Hq ? qs + h * p.D : h < p.Hq + p.Hkv ? ks + (h - p.Hq) * p.D : vs + (h - p.Hq - p.Hkv) * p.D;
+  };
+  auto target = [&](int h) {
+    return h < p.Hq              ? qd + h * p.D
+           : h < p.Hq + p.Hkv    ? k + cache + (h - p.Hq) * p.kv_hstride
+                                 : v + cache + (h - p.Hq - p.Hkv) * p.kv_hstride;
+  };
+  bool angles = false;
+  // items of a head in turn where a head has more than the threads of a row
+  for (int u0 = 0; u0 < p.items; u0 += blockDim.x) {
+    const int u = u0 + threadIdx.x;
+    const bool in = u < p.items, turn = u < p.pair_items;
+    // elements of the item's chunks: the two halves of its pairs, or two neighbours, or one that passes
+    const int e0 = turn ? (kInter ? 2 * u * VE : u * VE) : 2 * p.half + (u - p.pair_items) * VE;
+    const int e1 = kInter ? e0 + VE : e0 + p.half;
+    for (int h0 = threadIdx.y; h0 < heads || !angles; h0 += kBatch * blockDim.y) {
+      Chunk<Tin, VE> x[kBatch], y[kBatch];
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        const int h = h0 + i * blockDim.y;
+        if (in && h < heads) {
+          const Tin *s = source(h);
+          x[i] = load_chunk<Tin, VE>(s + e0);
+          if (turn) y[i] = load_chunk<Tin, VE>(s + e1);
+        }
+      }
+      if (!angles) {  // while the first loads are on their way
+        angles = true;
+        for (int i = tid; i < p.half; i += nthreads) {
+          const long long a = static_cast<long long>(static_cast<unsigned long long>(pos) * turns[i]);
+          float sn, cn;
+          sincospif(static_cast<float>(a) * 0x1p-63f, &sn, &cn);
+          cs[i] = make_float2(cn * p.magnitude, sn * p.magnitude);
+        }
+        __syncthreads();
+      }
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        const int h = h0 + i * blockDim.y;
+        if (!in || h >= heads) continue;
+        if (turn && h < p.Hq + p.Hkv) {
+          if constexpr (kInter) {  // VE == 1: (x, y); else pairs side by side in either chunk
+            if constexpr (VE == 1) {
+              const float2 c = cs[u];
+              const float a = to_f32(x[i].v[0]), bb = to_f32(y[i].v[0]);
+              x[i].v[0] = from_f32<Tin>(a * c.x - bb * c.y);
+              y[i].v[0] = from_f32<Tin>(a * c.y + bb * c.x);
+            } else {
+#pragma unroll
+              for (int e = 0; e < VE; e += 2) {
+                const float2 c = cs[u * VE + e / 2], c2 = cs[u * VE + VE / 2 + e / 2];
+                const float a = to_f32(x[i].v[e]), bb = to_f32(x[i].v[e + 1]);
+                x[i].v[e] = from_f32<Tin>(a * c.x - bb * c.y);
+                x[i].v[e + 1] = from_f32<Tin>(a * c.y + bb * c.x);
+                const float a2 = to_f32(y[i].v[e]), b2 = to_f32(y[i].v[e + 1]);
+                y[i].v[e] = from_f32<Tin>(a2 * c2.x - b2 * c2.y);
+                y[i].v[e + 1] = from_f32<Tin>(a2 * c2.y + b2 * c2.x);
+              }
+            }
+          } else {
+#pragma unroll
+            for (int e = 0; e < VE; ++e) {
+              const float2 c = cs[u * VE + e];
+              const float a = to_f32(x[i].v[e]), bb = to_f32(y[i].v[e]);
+              x[i].v[e] = from_f32<Tin>(a * c.x - bb * c.y);
+              y[i].v[e] = from_f32<Tin>(a * c.y + bb * c.x);
+            }
+          }
+        }
+        Tin *d = target(h);
+        store_chunk<Tin, VE>(d + e0, x[i]);
+        if (turn) store_chunk<Tin, VE>(d + e1, y[i]);
+      }
     }
-    if (u >= p.half) {
-      dst[u + p.half] = src[u + p.half];
-      continue;
-    }
-    const int i0 = p.interleaved ? 2 * u : u, i1 = p.interleaved ? 2 * u + 1 : u + p.half;
-    const Tin x = src[i0], y = src[i1];
-    if (!turn) {
-      dst[i0] = x;
-      dst[i1] = y;
-      continue;
-    }
-    const float xf = to_f32(x), yf = to_f32(y);
-    const float2 c = cs[u];
-    dst[i0] = from_f32<Tin>(xf * c.x - yf * c.y);
-    dst[i1] = from_f32<Tin>(xf * c.y + yf * c.x);
   }
 }
 
-template <typename Tin>
-cudaError_t rope_one(const RopeArgs &a, const RopeParams &p) {
-  return launch_pdl(rope_append_kernel<Tin>, dim3(static_cast<unsigned>(a.B) * a.T), dim3(kRopeThreads),
+template <typename Tin, int VE, bool kInter>
+cudaError_t rope_one(const RopeArgs &a, RopeParams p) {
+  p.pair_items = p.half / VE;  // two chunks each
+  p.items = p.pair_items + (p.D - 2 * p.half) / VE;
+  int bx = 1;
+  while (bx < p.items && bx < 256) bx *= 2;
+  const int heads = a.Hq + 2 * a.Hkv;
+  int by = 1;  // up to 512 threads, kBatch heads each
+  while (bx * by < 512 && by * kBatch < heads) by *= 2;
+  return launch_pdl(rope_append_kernel<Tin, VE, kInter>, dim3(static_cast<unsigned>(a.B) * a.T), dim3(bx, by),
                     static_cast<size_t>(p.half) * sizeof(float2), a.stream, static_cast<const Tin *>(a.q),
                     static_cast<const Tin *>(a.k_new), static_cast<const Tin *>(a.v_new),
                     static_cast<const unsigned long long *>(a.turns), a.kv_len, a.new_len, a.pos_offset,
@@ -116,10 +191,19 @@ cudaError_t rope_one(const RopeArgs &a, const RopeParams &p) {
                     static_cast<WsHeader *>(a.ws));
 }
 
+// Chunks of 16 bytes need both halves of the pairs to fall on chunk borders; element by element otherwise.
+template <typename Tin>
+cudaError_t rope_any(const RopeArgs &a, const RopeParams &p) {
+  constexpr int VE = 16 / sizeof(Tin);
+  const bool whole = p.half % VE == 0;
+  if (p.interleaved) return whole ? rope_one<Tin, VE, true>(a, p) : rope_one<Tin, 1, true>(a, p);
+  return whole ? rope_one<Tin, VE, false>(a, p) : rope_one<Tin, 1, false>(a, p);
+}
+
 }  // namespace
 
 cudaError_t launch_rope_append(const RopeArgs &a) {
-  RopeParams p;
+  RopeParams p{};
   p.T = a.T;
   p.Hq = a.Hq;
   p.Hkv = a.Hkv;
@@ -134,7 +218,7 @@ cudaError_t launch_rope_append(const RopeArgs &a) {
   p.kv_bstride = a.kv_batch_stride;
   p.kv_hstride = a.kv_head_stride;
   p.magnitude = a.magnitude;
-  return a.in_f32 ? rope_one<float>(a, p) : rope_one<__nv_bfloat16>(a, p);
+  return a.in_f32 ? rope_any<float>(a, p) : rope_any<__nv_bfloat16>(a, p);
 }
 
 }  // namespace mgd

@@ -9,14 +9,15 @@
 // ascending unsigned number, then the complement of the index, so no two keys
 // are equal and ties need no rule of their own.
 //
-// Bound by HBM.  A cluster of up to 8 CTAs shares a row; each thread holds 32
-// entries of its CTA's part in registers, folds them into its own running
-// (m, Z, W), counts those before the token, and the CTA looks for alternatives only
-// among entries that can be one: of the 64 groups of 4 threads, each with its
-// largest value, the K-th largest of these values bounds the K-th best entry from
-// below, so a handful more than K entries are left to be put in order.  (Where ties
-// or sorted rows leave more than the list holds, the CTA takes the maximum K times.)
-// The parts meet in the first CTA's shared memory.
+// Bound by HBM.  A cluster of up to 8 CTAs shares a row.  Each thread holds 128 bytes
+// of its CTA's part in registers, folds them into its own running sums (relative to its
+// own maximum), counts those before the token, and puts aside
+// those that can be alternatives: of the 64 groups of 4 threads, each with its largest
+// value, the K-th largest of these values bounds the K-th best entry from below, so a
+// handful more than K entries of the first block are put aside, and of later ones those
+// above that bound.  A list that has grown is put in order and cut to the best K, which
+// raises the bound.  (Where ties or sorted rows leave more than the list holds, the CTA
+// takes the maximum K times.)  The parts meet in the first CTA's shared memory.
 #include <algorithm>
 
 #include "common.cuh"
@@ -26,13 +27,14 @@ namespace {
 
 constexpr int kLpThreads = 256;
 constexpr int kLpCtas = 3;                        // CTAs of an SM
-constexpr int kLpHeld = 32;                       // entries a thread holds at once
-constexpr int kLpBlock = kLpThreads * kLpHeld;    // entries a CTA holds at once
-constexpr int kLpGroups = 64;                     // groups of threads, the candidates for the bound below
-constexpr int kLpList = 512;                      // entries that may be put in order at once
+constexpr int kLpLoads = 8;                       // 16-byte loads of a thread at once
+constexpr int kLpGroups = 64;                     // groups of threads, the candidates for the bound
+constexpr int kLpList = 512;                      // entries put aside
+constexpr int kLpCut = 96;                        // a list longer than this is cut to the best K
 constexpr int kLpMaxK = 32;                       // kLpGroups bounds it
 constexpr int kLpMaxCluster = 8;
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
 
 __device__ __forceinline__ unsigned long long order_key(float x, unsigned j) {
   const unsigned b = __float_as_uint(x + 0.f);  // -0 and +0 are one value
@@ -50,15 +52,15 @@ __device__ __forceinline__ float fmax3_nan(float a, float b, float c) {
   return d;
 }
 
-// What a CTA knows of a row.
+// What a CTA knows of a row: with y = (x - m) log2(e)
 struct RowPart {
-  float m, z, w;   // maximum, sum e^{x - m}, sum e^{x - m} (x - m)
+  float m, z, w;   // the maximum; z = sum 2^y, w = sum 2^y y
   int before;      // entries before the token
   int none;        // a NaN or +inf was seen
   int pad[3];
 };
 struct LpShared {
-  unsigned long long list[kLpList];             // entries that may be alternatives
+  unsigned long long list[kLpList + 2];         // entries put aside
   unsigned long long best[kLpMaxK];             // the best so far, in order
   unsigned long long red[kLpThreads / 32];
   unsigned long long all[kLpMaxCluster][kLpMaxK];  // of every CTA, in the first one's shared memory
@@ -69,44 +71,95 @@ struct LpShared {
   int count;
 };
 
-// One 16-byte chunk of logits as floats.
+// Chunks of 16 bytes: entry e as a float, the largest entry (NaN if there is one), and the entries above
+// a threshold.
 template <typename Tin>
-__device__ __forceinline__ void unpack(const uint4 &c, float *x);
+struct Entries;
 template <>
-__device__ __forceinline__ void unpack<float>(const uint4 &c, float *x) {
-  x[0] = __uint_as_float(c.x);
-  x[1] = __uint_as_float(c.y);
-  x[2] = __uint_as_float(c.z);
-  x[3] = __uint_as_float(c.w);
-}
-template <>
-__device__ __forceinline__ void unpack<__nv_bfloat16>(const uint4 &c, float *x) {
-  const unsigned w[4] = {c.x, c.y, c.z, c.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    x[2 * i] = __uint_as_float(w[i] << 16);
-    x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+struct Entries<float> {
+  static constexpr int kPer = 4;
+  static __device__ __forceinline__ uint4 none() { return make_uint4(0xFF800000u, 0xFF800000u, 0xFF800000u, 0xFF800000u); }
+  static __device__ __forceinline__ float2 pair(const uint4 &c, int i) {
+    return i == 0 ? make_float2(__uint_as_float(c.x), __uint_as_float(c.y))
+                  : make_float2(__uint_as_float(c.z), __uint_as_float(c.w));
   }
+  static __device__ __forceinline__ float largest(const uint4 (&c)[kLpLoads]) {
+    float m[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+    for (int i = 0; i < kLpLoads; ++i) {
+      m[0] = fmax3_nan(m[0], __uint_as_float(c[i].x), __uint_as_float(c[i].y));
+      m[1] = fmax3_nan(m[1], __uint_as_float(c[i].z), __uint_as_float(c[i].w));
+    }
+    return fmax3_nan(m[0], m[1], m[1]);
+  }
+  static __device__ __forceinline__ int above(const uint4 &c, float t) {
+    return (__uint_as_float(c.x) > t) + (__uint_as_float(c.y) > t) + (__uint_as_float(c.z) > t) +
+           (__uint_as_float(c.w) > t);
+  }
+};
+template <>
+struct Entries<__nv_bfloat16> {
+  static constexpr int kPer = 8;
+  static __device__ __forceinline__ uint4 none() { return make_uint4(0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u); }
+  static __device__ __forceinline__ float2 pair(const uint4 &c, int i) {
+    const unsigned w = i == 0 ? c.x : i == 1 ? c.y : i == 2 ? c.z : c.w;
+    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+  }
+  static __device__ __forceinline__ __nv_bfloat162 two(unsigned w) { return *reinterpret_cast<const __nv_bfloat162 *>(&w); }
+  static __device__ __forceinline__ float largest(const uint4 (&c)[kLpLoads]) {
+    __nv_bfloat162 m[2] = {two(c[0].x), two(c[0].y)};
+#pragma unroll
+    for (int i = 0; i < kLpLoads; ++i) {
+      m[0] = __hmax2_nan(m[0], __hmax2_nan(two(c[i].x), two(c[i].z)));
+      m[1] = __hmax2_nan(m[1], __hmax2_nan(two(c[i].y), two(c[i].w)));
+    }
+    const float2 a = __bfloat1622float2(__hmax2_nan(m[0], m[1]));
+    return fmax3_nan(a.x, a.y, a.y);
+  }
+  // the threshold is a bfloat16 value; the count of a chunk (at most 8) is exact in bfloat16
+  static __device__ __forceinline__ int above(const uint4 &c, float t) {
+    const __nv_bfloat162 tt = __float2bfloat162_rn(t);
+    const __nv_bfloat162 n = __hadd2(__hadd2(__hgt2(two(c.x), tt), __hgt2(two(c.y), tt)),
+                                     __hadd2(__hgt2(two(c.z), tt), __hgt2(two(c.w), tt)));
+    const float2 f = __bfloat1622float2(n);
+    return static_cast<int>(f.x + f.y);
+  }
+};
+
+// The next value below a finite one (or +-0) of the type.
+template <typename Tin>
+__device__ __forceinline__ float below(float x) {
+  const unsigned step = sizeof(Tin) == 2 ? 0x10000u : 1u;
+  const unsigned b = __float_as_uint(x + 0.f);
+  return __uint_as_float(b == 0u ? 0x80000000u + step : (b & 0x80000000u) ? b + step : b - step);
 }
 
 __device__ __forceinline__ void fold(RowPart &a, const RowPart &b) {
   const float m = fmaxf(a.m, b.m);
   if (m == -INFINITY) return;
-  const float da = a.m - m, db = b.m - m;  // -inf for a side without a finite entry: its sums are 0
-  const float ea = da == -INFINITY ? 0.f : expf(da), eb = db == -INFINITY ? 0.f : expf(db);
+  const float da = (a.m - m) * kLog2e, db = (b.m - m) * kLog2e;  // -inf for a side without a finite entry
+  const float ea = exp2f(da), eb = exp2f(db);
   const float wa = ea > 0.f ? a.w + a.z * da : 0.f, wb = eb > 0.f ? b.w + b.z * db : 0.f;
   a.w = wa * ea + wb * eb;
   a.z = a.z * ea + b.z * eb;
   a.m = m;
 }
 
-// The n keys of `from` in descending order into `to`, at most K of them: each key's place is the number
-// of larger ones.  Ends with a barrier.
-__device__ __forceinline__ void put_in_order(const unsigned long long *from, int n, unsigned long long *to, int K) {
+// The n keys of `from` (room for one more) in descending order into `to`, at most K of them, which are
+// cleared first: each key's place is the number of larger ones.  Every thread takes part; begins and ends
+// with a barrier.
+__device__ __forceinline__ void put_in_order(unsigned long long *from, int n, unsigned long long *to, int K) {
+  if (threadIdx.x < K) to[threadIdx.x] = 0;
+  if (threadIdx.x == 0) from[n] = 0;
+  __syncthreads();
   for (int i = threadIdx.x; i < n; i += kLpThreads) {
     const unsigned long long mine = from[i];
     int place = 0;
-    for (int j = 0; j < n; ++j) place += from[j] > mine;
+#pragma unroll 4
+    for (int j = 0; j < n; j += 2) {
+      const ulonglong2 two = *reinterpret_cast<const ulonglong2 *>(from + j);
+      place += (two.x > mine) + (two.y > mine);
+    }
     if (mine != 0 && place < K) to[place] = mine;
   }
   __syncthreads();
@@ -117,11 +170,12 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas)
     logprobs_kernel(const Tin *__restrict__ logits, int64_t stride, const int32_t *__restrict__ tokens, int R, int V,
                     int K, float *__restrict__ logprob, float *__restrict__ entropy, int32_t *__restrict__ rank,
                     int32_t *__restrict__ top_ids, float *__restrict__ top_lp, WsHeader *hdr) {
-  constexpr int VE = 16 / sizeof(Tin), NCH = kLpHeld / VE;  // entries of a chunk, chunks a thread holds
+  using En = Entries<Tin>;
+  constexpr int VE = En::kPer;  // entries of a chunk
   constexpr int kPerGroup = kLpThreads / kLpGroups;
   pdl_launch_dependents();
   pdl_wait();
-  __shared__ LpShared sh;
+  __shared__ __align__(16) LpShared sh;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int C = gridDim.x, part = blockIdx.x;  // the cluster spans the grid's x
   if (part == 0 && blockIdx.y == 0) {
@@ -159,8 +213,10 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas)
     if (part == 0 && tid < head + tail) edge = tid < head ? tid : V - tail + (tid - head);
     const int per = (chunks + C - 1) / C;
     const int c0 = min(part * per, chunks), c1 = min(c0 + per, chunks);
+    const int tok_chunk = tok >= head && tok < V - tail && (tok - head) / VE < c1 ? (tok - head) / VE : -1;
     if (tid == 0) sh.count = 0;
-    if (tid < K) sh.best[tid] = 0;
+    // entries above this count as before the token: with an index below its own, equal ones too
+    const float xt_before = xt == -INFINITY ? xt : below<Tin>(xt);
 
     RowPart me;
     me.m = -INFINITY;
@@ -168,38 +224,19 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas)
     me.before = 0;
     me.none = 0;
     float floor = -INFINITY;  // value that an alternative of this CTA has at least
-    for (int base = c0; base < c1 || base == c0; base += kLpThreads * NCH) {
-      float x[kLpHeld];
-      {
-        uint4 raw[NCH];
+    for (int base = c0; base < c1 || base == c0; base += kLpThreads * kLpLoads) {
+      uint4 x[kLpLoads];
 #pragma unroll
-        for (int i = 0; i < NCH; ++i) {
-          const int c = base + i * kLpThreads + tid;
-          if (c < c1) raw[i] = __ldcs(reinterpret_cast<const uint4 *>(x0 + head) + c);
-        }
-#pragma unroll
-        for (int i = 0; i < NCH; ++i) {
-          const int c = base + i * kLpThreads + tid;
-          unpack<Tin>(raw[i], x + i * VE);
-          if (c >= c1) {
-#pragma unroll
-            for (int e = 0; e < VE; ++e) x[i * VE + e] = -INFINITY;
-          }
-        }
+      for (int i = 0; i < kLpLoads; ++i) {
+        const int c = base + i * kLpThreads + tid;
+        x[i] = c < c1 ? __ldcs(reinterpret_cast<const uint4 *>(x0 + head) + c) : En::none();
       }
       const float ex = (edge >= 0 && base == c0) ? to_f32(x0[edge]) : -INFINITY;
-      float mx[2] = {ex, -INFINITY};
-#pragma unroll
-      for (int e = 0; e < kLpHeld; e += 4) {
-        mx[0] = fmax3_nan(mx[0], x[e], x[e + 1]);
-        mx[1] = fmax3_nan(mx[1], x[e + 2], x[e + 3]);
-      }
-      const float top = fmax3_nan(mx[0], mx[1], mx[1]);
+      const float inner = En::largest(x), top = fmax3_nan(inner, ex, ex);
       me.none |= !(top < INFINITY);
       // ---- sums, relative to the thread's own maximum
       if (top > me.m) {
-        const float d = me.m - top;  // -inf at first: nothing is there yet
-        const float e = d == -INFINITY ? 0.f : ex2(d * kLog2e);
+        const float d = (me.m - top) * kLog2e, e = ex2(d);  // -inf and 0 at first: nothing is there yet
         me.w = e > 0.f ? (me.w + me.z * d) * e : 0.f;
         me.z *= e;
         me.m = top;
@@ -207,112 +244,95 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas)
       const float mu = me.m == -INFINITY ? 0.f : me.m;
       const float2 nm = make_float2(-mu, -mu), l2 = make_float2(kLog2e, kLog2e);
       float2 z = make_float2(0.f, 0.f), w = make_float2(0.f, 0.f);
-#pragma unroll
-      for (int e = 0; e < kLpHeld; e += 2) {
-        float2 d = __fadd2_rn(make_float2(x[e], x[e + 1]), nm);
-        d.x = fmaxf(d.x, -200.f);  // its exponential is 0, and so is the product with it
-        d.y = fmaxf(d.y, -200.f);
-        const float2 y = __fmul2_rn(d, l2);
+      auto add = [&](float2 v) {
+        float2 y = __fmul2_rn(__fadd2_rn(v, nm), l2);
+        y.x = fmaxf(y.x, -300.f);  // 2^y is 0 there, and so is the product with it
+        y.y = fmaxf(y.y, -300.f);
         const float2 p = make_float2(ex2(y.x), ex2(y.y));
         z = __fadd2_rn(z, p);
-        w = __ffma2_rn(p, d, w);
+        w = __ffma2_rn(p, y, w);
+      };
+#pragma unroll
+      for (int i = 0; i < kLpLoads; ++i) {
+#pragma unroll
+        for (int e = 0; e < VE / 2; ++e) add(En::pair(x[i], e));
+        // ---- entries before the token
+        const int j0 = head + (base + i * kLpThreads + tid) * VE;
+        if (xt == -INFINITY && j0 + VE <= tok)  // nothing is below: every entry counts
+          me.before += base + i * kLpThreads + tid < c1 ? VE : 0;
+        else
+          me.before += En::above(x[i], j0 + VE <= tok ? xt_before : xt);
+      }
+      if (tok_chunk >= base && tok_chunk < base + kLpThreads * kLpLoads && (tok_chunk - base) % kLpThreads == tid)
+        for (int j = head + tok_chunk * VE; j < tok; ++j)  // of the token's own chunk, equal entries before it
+          me.before += to_f32(x0[j]) == xt;
+      if (edge >= 0 && base == c0) {
+        add(make_float2(ex, -INFINITY));
+        me.before += ex > xt || (ex == xt && edge < tok);
       }
       me.z += z.x + z.y;
       me.w += w.x + w.y;
-      if (edge >= 0 && base == c0) {
-        const float d = fmaxf(ex - mu, -200.f), p = ex2(d * kLog2e);
-        me.z += p;
-        me.w += p * d;
-        me.before += ex > xt || (ex == xt && edge < tok);
-      }
-      // ---- entries before the token: of equal values those with a lower index
-#pragma unroll
-      for (int i = 0; i < NCH; ++i) {
-        const int j0 = head + (base + i * kLpThreads + tid) * VE;
-        if (j0 + VE <= tok) {
-#pragma unroll
-          for (int e = 0; e < VE; ++e) me.before += x[i * VE + e] >= xt;
-        } else {
-#pragma unroll
-          for (int e = 0; e < VE; ++e) me.before += x[i * VE + e] > xt;
-          if (j0 < tok) {  // the token's own chunk
-#pragma unroll
-            for (int e = 0; e < VE; ++e) me.before += x[i * VE + e] == xt && j0 + e < tok;
-          }
-        }
-      }
-      // entries past this CTA's part are -inf: none of them counts, unless the token itself is -inf
-      if (xt == -INFINITY) {
-#pragma unroll
-        for (int i = 0; i < NCH; ++i) {
-          const int c = base + i * kLpThreads + tid, j0 = head + c * VE;
-          if (c >= c1)
-#pragma unroll
-            for (int e = 0; e < VE; ++e) me.before -= j0 + e < tok;
-        }
-      }
       if (K == 0) continue;
       // ---- alternatives
-      float g = top;
+      if (base == c0) {  // the bound that the first block gives
+        float g = top;
 #pragma unroll
-      for (int o = 1; o < kPerGroup; o <<= 1) g = fmaxf(g, __shfl_xor_sync(0xffffffffu, g, o));
-      __syncthreads();  // the list of the entries before this block has been used
-      if (tid % kPerGroup == 0) sh.group[tid / kPerGroup] = g;
-      __syncthreads();
-      if (tid < kLpGroups) {
-        const float mine = sh.group[tid];
-        int place = 0;
-        for (int j = 0; j < kLpGroups; ++j) place += sh.group[j] > mine || (sh.group[j] == mine && j < tid);
-        if (place == K - 1) sh.floor = fmaxf(mine, floor);
-      }
-      __syncthreads();
-      floor = sh.floor;
-      if (top >= floor && top > -INFINITY) {
-#pragma unroll
-        for (int i = 0; i < NCH; ++i) {
-          const int j0 = head + (base + i * kLpThreads + tid) * VE;
-#pragma unroll
-          for (int e = 0; e < VE; ++e)
-            if (x[i * VE + e] >= floor && x[i * VE + e] > -INFINITY) {
-              const int at = atomicAdd(&sh.count, 1);
-              if (at < kLpList - kLpMaxK) sh.list[at] = order_key(x[i * VE + e], j0 + e);
-            }
+        for (int o = 1; o < kPerGroup; o <<= 1) g = fmaxf(g, __shfl_xor_sync(0xffffffffu, g, o));
+        if (tid % kPerGroup == 0) sh.group[tid / kPerGroup] = g;
+        __syncthreads();
+        if (tid < kLpGroups) {
+          const float mine = sh.group[tid];
+          int place = 0;
+#pragma unroll 8
+          for (int j = 0; j < kLpGroups; ++j) place += sh.group[j] > mine || (sh.group[j] == mine && j < tid);
+          if (place == K - 1) sh.floor = mine;
         }
-        if (edge >= 0 && base == c0 && ex >= floor && ex > -INFINITY) {
+        __syncthreads();
+        floor = sh.floor;
+      }
+      int over = 0;
+      if (top >= floor && top > -INFINITY) {  // few threads: which entries, then those one by one, read again
+        unsigned long long which = 0;
+#pragma unroll
+        for (int i = 0; i < kLpLoads; ++i)
+#pragma unroll
+          for (int e = 0; e < VE; ++e) {
+            const float2 v = En::pair(x[i], e / 2);
+            which |= static_cast<unsigned long long>((e % 2 ? v.y : v.x) >= floor) << (i * VE + e);
+          }
+        auto aside = [&](int j) {
+          const float v = to_f32(x0[j]);
+          if (v == -INFINITY) return;
           const int at = atomicAdd(&sh.count, 1);
-          if (at < kLpList - kLpMaxK) sh.list[at] = order_key(ex, edge);
+          if (at < kLpList)
+            sh.list[at] = order_key(v, j);
+          else
+            over = 1;
+        };
+        for (; which; which &= which - 1) {
+          const int bit = __ffsll(which) - 1, c = base + bit / VE * kLpThreads + tid;
+          if (c < c1) aside(head + c * VE + bit % VE);
         }
+        if (edge >= 0 && base == c0 && ex >= floor) aside(edge);
       }
-      __syncthreads();
+      over = __syncthreads_or(over);
       const int n = sh.count;
-      if (n <= kLpList - kLpMaxK) {
-        // the best so far go behind them, and all are put in order
-        if (tid < K) sh.list[n + tid] = sh.best[tid];
-        __syncthreads();
-        if (tid < K) sh.best[tid] = 0;
-        if (tid == 0) sh.count = 0;
-        __syncthreads();
-        put_in_order(sh.list, n + K, sh.best, K);
-      } else {
-        // too many are level: the largest key below the last one, K times
-        if (tid < K) sh.list[tid] = sh.best[tid];
-        unsigned long long below = ~0ull;
-        __syncthreads();
+      if (over) {
+        // more than the list holds: the largest key below the last one, K times, of this block and of what
+        // the list had before it (entries of this block that are in the list count once: keys are unique)
+        unsigned long long last = ~0ull;
         for (int k = 0; k < K; ++k) {
-          unsigned long long b = tid < K && sh.list[tid] < below ? sh.list[tid] : 0;
-#pragma unroll
-          for (int i = 0; i < NCH; ++i) {
-            const int j0 = head + (base + i * kLpThreads + tid) * VE;
-#pragma unroll
-            for (int e = 0; e < VE; ++e) {
-              const unsigned long long key = x[i * VE + e] > -INFINITY ? order_key(x[i * VE + e], j0 + e) : 0;
-              if (key < below && key > b) b = key;
-            }
+          unsigned long long b = 0;
+          auto see = [&](unsigned long long key) {
+            if (key < last && key > b) b = key;
+          };
+          for (int i = tid; i < kLpList; i += kLpThreads) see(sh.list[i]);
+          const int e1 = head + min(base + kLpThreads * kLpLoads, c1) * VE;
+          for (int j = head + base * VE + tid; j < e1; j += kLpThreads) {
+            const float v = to_f32(x0[j]);
+            if (v > -INFINITY) see(order_key(v, j));
           }
-          if (edge >= 0 && base == c0 && ex > -INFINITY) {
-            const unsigned long long key = order_key(ex, edge);
-            if (key < below && key > b) b = key;
-          }
+          if (edge >= 0 && base == c0 && ex > -INFINITY) see(order_key(ex, edge));
           for (int o = 16; o; o >>= 1) {
             const unsigned long long y = __shfl_xor_sync(0xffffffffu, b, o);
             b = y > b ? y : b;
@@ -322,13 +342,22 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas)
           b = 0;
           for (int i = 0; i < kLpThreads / 32; ++i) b = sh.red[i] > b ? sh.red[i] : b;
           if (tid == 0) sh.best[k] = b;
-          below = b;
+          last = b;
           __syncthreads();
         }
-        if (tid == 0) sh.count = 0;
+      } else if (n > kLpCut) {
+        put_in_order(sh.list, n, sh.best, K);
+      } else {
+        __syncthreads();  // the count has been read by all
+        continue;
       }
+      // the best K are the list now
+      if (tid < K) sh.list[tid] = sh.best[tid];
+      if (tid == 0) sh.count = K;
       if (sh.best[K - 1] != 0) floor = fmaxf(floor, key_value(sh.best[K - 1]));
+      __syncthreads();
     }
+    if (K > 0) put_in_order(sh.list, sh.count, sh.best, K);
     // ---- this CTA's part
     for (int o = 16; o; o >>= 1) {
       RowPart y;
@@ -377,24 +406,21 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas)
         r.none |= o.none;
       }
       const bool none = r.none || r.m == -INFINITY;
-      const float lz = logf(r.z);
+      const float lz = log2f(r.z);  // in units of log2, as r.w
       if (tid == 0) {
-        logprob[row] = none ? __int_as_float(0x7FFFFFFF) : (xt - r.m) - lz;
-        entropy[row] = none ? __int_as_float(0x7FFFFFFF) : lz - r.w / r.z;
+        logprob[row] = none ? __int_as_float(0x7FFFFFFF) : (xt - r.m) - lz * kLn2;
+        entropy[row] = none ? __int_as_float(0x7FFFFFFF) : (lz - r.w / r.z) * kLn2;
         rank[row] = none ? -1 : r.before;
       }
       if (K > 0) {
         if (C > 1) {
           for (int i = tid; i < C * K; i += kLpThreads) sh.list[i] = sh.all[i / K][i % K];
-          __syncthreads();
-          if (tid < K) sh.best[tid] = 0;
-          __syncthreads();
           put_in_order(sh.list, C * K, sh.best, K);
         }
         if (tid < K) {
           const unsigned long long key = none ? 0 : sh.best[tid];
           top_ids[row * K + tid] = key ? static_cast<int32_t>(0xFFFFFFFFu - static_cast<unsigned>(key)) : -1;
-          top_lp[row * K + tid] = key ? (key_value(key) - r.m) - lz : -INFINITY;
+          top_lp[row * K + tid] = key ? (key_value(key) - r.m) - lz * kLn2 : -INFINITY;
         }
       }
     }
@@ -411,7 +437,7 @@ cudaError_t logprobs_one(const LogprobArgs &a) {
   // CTAs a row: as many as the row fills, up to 8, for few rows; with many rows fewer and longer parts,
   // as long as about eight waves of CTAs are left to even out the ends.
   int C = 1;
-  while (C < kLpMaxCluster && a.V > C * (kLpBlock / 4)) C *= 2;
+  while (C < kLpMaxCluster && a.V > C * kLpThreads * kLpLoads * 2) C *= 2;
   while (C > 1 && static_cast<int64_t>(a.R) * (C / 2) >= 8LL * kLpCtas * current_sm_count()) C /= 2;
   return launch_pdl_cluster(logprobs_kernel<Tin>, dim3(C, std::min(a.R, 65535)), dim3(kLpThreads), dim3(C), 0, a.stream,
                             static_cast<const Tin *>(a.logits), a.row_stride, a.tokens, a.R, a.V, a.K, a.logprob,

@@ -9,8 +9,10 @@
 // ascending unsigned number, then the complement of the index, so no two keys
 // are equal and ties need no rule of their own.
 //
-// Bound by HBM.  A cluster of up to 8 CTAs shares a row.  Each thread holds 128 bytes
-// of its CTA's part in registers, folds them into its own running sums (relative to its
+// Bound by HBM.  A cluster of up to 8 CTAs shares a row, and the clusters that fit the GPU
+// walk the rows.  Blocks of 32 KB come by bulk copies into two stages of shared memory,
+// the next two on their way whatever the CTA is at, across rows as well.  Each thread
+// takes 128 bytes of a block, folds them into its own running sums (relative to its
 // own maximum), counts those before the token, and puts aside
 // those that can be alternatives: of the 64 groups of 4 threads, each with its largest
 // value, the K-th largest of these values bounds the K-th best entry from below, so a
@@ -27,7 +29,10 @@ namespace {
 
 constexpr int kLpThreads = 256;
 constexpr int kLpCtas = 3;                        // CTAs of an SM
-constexpr int kLpLoads = 8;                       // 16-byte loads of a thread at once
+constexpr int kLpLoads = 8;                       // 16-byte chunks of a thread in a block
+constexpr int kLpChunks = kLpThreads * kLpLoads;  // chunks of a block
+constexpr int kLpStages = 2;
+constexpr int kLpStageBytes = kLpChunks * 16;
 constexpr int kLpGroups = 64;                     // groups of threads, the candidates for the bound
 constexpr int kLpList = 512;                      // entries put aside
 constexpr int kLpCut = 96;                        // a list longer than this is cut to the best K
@@ -69,10 +74,30 @@ struct LpShared {
   float group[kLpGroups];
   float floor;     // no alternative is below this value
   int count;
+  uint64_t full[kLpStages];  // mbarriers: a block has landed
+  int gave_up;
 };
 
-// Chunks of 16 bytes: entry e as a float, the largest entry (NaN if there is one), and the entries above
-// a threshold.
+// Where a row's parts lie: whole 16-byte chunks between `head` and `tail` single entries, chunks
+// [c0, c1) of them this CTA's.
+template <typename Tin>
+struct RowPlace {
+  const Tin *x;
+  int head, tail, c0, c1;
+  __device__ __forceinline__ RowPlace(const Tin *row, int V, int C, int part) : x(row) {
+    constexpr int VE = 16 / sizeof(Tin);
+    head = min(V, static_cast<int>(((16u - (reinterpret_cast<uintptr_t>(row) & 15u)) & 15u) / sizeof(Tin)));
+    const int chunks = (V - head) / VE;
+    tail = V - head - chunks * VE;
+    const int per = (chunks + C - 1) / C;
+    c0 = min(part * per, chunks);
+    c1 = min(c0 + per, chunks);
+  }
+  __device__ __forceinline__ int blocks() const { return (c1 - c0 + kLpChunks - 1) / kLpChunks; }
+};
+
+// Chunks of 16 bytes: a pair of entries as floats, the largest entry of a thread's chunks (NaN if there is
+// one) and of one chunk, and the number of entries above a threshold.
 template <typename Tin>
 struct Entries;
 template <>
@@ -83,7 +108,7 @@ struct Entries<float> {
     return i == 0 ? make_float2(__uint_as_float(c.x), __uint_as_float(c.y))
                   : make_float2(__uint_as_float(c.z), __uint_as_float(c.w));
   }
-  static __device__ __forceinline__ float largest(const uint4 (&c)[kLpLoads]) {
+  static __device__ __forceinline__ float largest_nan(const uint4 (&c)[kLpLoads]) {
     float m[2] = {-INFINITY, -INFINITY};
 #pragma unroll
     for (int i = 0; i < kLpLoads; ++i) {
@@ -92,9 +117,14 @@ struct Entries<float> {
     }
     return fmax3_nan(m[0], m[1], m[1]);
   }
-  static __device__ __forceinline__ int above(const uint4 &c, float t) {
-    return (__uint_as_float(c.x) > t) + (__uint_as_float(c.y) > t) + (__uint_as_float(c.z) > t) +
-           (__uint_as_float(c.w) > t);
+  // entries above a threshold, summed over the chunks of a block
+  using Count = int;
+  static __device__ __forceinline__ void above(Count &n, const uint4 &c, float t) {
+    n += (__uint_as_float(c.x) > t) + (__uint_as_float(c.y) > t) + (__uint_as_float(c.z) > t) + (__uint_as_float(c.w) > t);
+  }
+  static __device__ __forceinline__ int total(Count n) { return n; }
+  static __device__ __forceinline__ float largest(const uint4 &c) {
+    return fmaxf(fmaxf(__uint_as_float(c.x), __uint_as_float(c.y)), fmaxf(__uint_as_float(c.z), __uint_as_float(c.w)));
   }
 };
 template <>
@@ -106,7 +136,7 @@ struct Entries<__nv_bfloat16> {
     return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
   }
   static __device__ __forceinline__ __nv_bfloat162 two(unsigned w) { return *reinterpret_cast<const __nv_bfloat162 *>(&w); }
-  static __device__ __forceinline__ float largest(const uint4 (&c)[kLpLoads]) {
+  static __device__ __forceinline__ float largest_nan(const uint4 (&c)[kLpLoads]) {
     __nv_bfloat162 m[2] = {two(c[0].x), two(c[0].y)};
 #pragma unroll
     for (int i = 0; i < kLpLoads; ++i) {
@@ -116,13 +146,23 @@ struct Entries<__nv_bfloat16> {
     const float2 a = __bfloat1622float2(__hmax2_nan(m[0], m[1]));
     return fmax3_nan(a.x, a.y, a.y);
   }
-  // the threshold is a bfloat16 value; the count of a chunk (at most 8) is exact in bfloat16
-  static __device__ __forceinline__ int above(const uint4 &c, float t) {
+  // in pairs of bfloat16: the threshold is a bfloat16 value, and a block's count, at most 32 in either
+  // half, is exact in bfloat16
+  struct Count {
+    __nv_bfloat162 n = __float2bfloat162_rn(0.f);
+  };
+  static __device__ __forceinline__ void above(Count &n, const uint4 &c, float t) {
     const __nv_bfloat162 tt = __float2bfloat162_rn(t);
-    const __nv_bfloat162 n = __hadd2(__hadd2(__hgt2(two(c.x), tt), __hgt2(two(c.y), tt)),
-                                     __hadd2(__hgt2(two(c.z), tt), __hgt2(two(c.w), tt)));
-    const float2 f = __bfloat1622float2(n);
+    n.n = __hadd2(n.n, __hadd2(__hadd2(__hgt2(two(c.x), tt), __hgt2(two(c.y), tt)),
+                               __hadd2(__hgt2(two(c.z), tt), __hgt2(two(c.w), tt))));
+  }
+  static __device__ __forceinline__ int total(const Count &n) {
+    const float2 f = __bfloat1622float2(n.n);
     return static_cast<int>(f.x + f.y);
+  }
+  static __device__ __forceinline__ float largest(const uint4 &c) {
+    const float2 a = __bfloat1622float2(__hmax2(__hmax2(two(c.x), two(c.y)), __hmax2(two(c.z), two(c.w))));
+    return fmaxf(a.x, a.y);
   }
 };
 
@@ -176,6 +216,7 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas)
   pdl_launch_dependents();
   pdl_wait();
   __shared__ __align__(16) LpShared sh;
+  extern __shared__ __align__(128) unsigned char stages[];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int C = gridDim.x, part = blockIdx.x;  // the cluster spans the grid's x
   if (part == 0 && blockIdx.y == 0) {
@@ -188,6 +229,33 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas)
       hdr->err[1] = 0u;
     }
   }
+  if (tid == 0) {
+    for (int i = 0; i < kLpStages; ++i) mbar_init(&sh.full[i], 1);
+    fence_mbar_init();
+    sh.gave_up = 0;
+  }
+  __syncthreads();
+  // thread 0 is two blocks ahead: its place in the sequence of rows with a token and their blocks
+  int64_t ahead = blockIdx.y;
+  int ahead_block = 0, issued = 0;
+  auto issue = [&] {
+    for (; ahead < R; ahead += gridDim.y, ahead_block = 0) {
+      const int t = tokens[ahead];
+      if (t < 0 || t >= V) continue;
+      const RowPlace<Tin> p(logits + ahead * stride, V, C, part);
+      if (ahead_block >= p.blocks()) continue;
+      const int c = p.c0 + ahead_block * kLpChunks;
+      const uint32_t bytes = 16u * min(kLpChunks, p.c1 - c);
+      const int st = issued++ % kLpStages;
+      mbar_arrive_expect_tx(&sh.full[st], bytes);
+      bulk_load(stages + st * kLpStageBytes, reinterpret_cast<const uint4 *>(p.x + p.head) + c, bytes, &sh.full[st]);
+      ++ahead_block;
+      return;
+    }
+  };
+  if (tid == 0)
+    for (int i = 0; i < kLpStages; ++i) issue();
+  int taken = 0;  // blocks used
   for (int64_t row = blockIdx.y; row < R; row += gridDim.y) {
     const int tok = tokens[row];
     if (tok < 0 || tok >= V) {  // no token (the whole cluster sees that)
@@ -204,15 +272,15 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas)
       }
       continue;
     }
-    const Tin *x0 = logits + row * stride;
+    const RowPlace<Tin> at(logits + row * stride, V, C, part);
+    const Tin *x0 = at.x;
+    const int head = at.head, tail = at.tail, c0 = at.c0, c1 = at.c1;
     const float xt = to_f32(x0[tok]);
-    // entries before and after the row's whole 16-byte chunks: the first CTA's first threads hold one each
-    const int head = min(V, static_cast<int>(((16u - (reinterpret_cast<uintptr_t>(x0) & 15u)) & 15u) / sizeof(Tin)));
-    const int chunks = (V - head) / VE, tail = V - head - chunks * VE;
+    // the entries outside of whole chunks: the first CTA's first threads hold one each
     int edge = -1;  // index of that entry
     if (part == 0 && tid < head + tail) edge = tid < head ? tid : V - tail + (tid - head);
-    const int per = (chunks + C - 1) / C;
-    const int c0 = min(part * per, chunks), c1 = min(c0 + per, chunks);
+    // chunks below tok_after lie before the token as a whole
+    const int tok_after = tok >= head ? (tok - head) / VE : 0;
     const int tok_chunk = tok >= head && tok < V - tail && (tok - head) / VE < c1 ? (tok - head) / VE : -1;
     if (tid == 0) sh.count = 0;
     // entries above this count as before the token: with an index below its own, equal ones too
@@ -224,15 +292,20 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas)
     me.before = 0;
     me.none = 0;
     float floor = -INFINITY;  // value that an alternative of this CTA has at least
-    for (int base = c0; base < c1 || base == c0; base += kLpThreads * kLpLoads) {
+    for (int base = c0; base < c1 || base == c0; base += kLpChunks) {
       uint4 x[kLpLoads];
-#pragma unroll
-      for (int i = 0; i < kLpLoads; ++i) {
-        const int c = base + i * kLpThreads + tid;
-        x[i] = c < c1 ? __ldcs(reinterpret_cast<const uint4 *>(x0 + head) + c) : En::none();
+      const unsigned char *st = stages + taken % kLpStages * kLpStageBytes;
+      if (base < c1) {
+        if (!mbar_wait(&sh.full[taken % kLpStages], (taken / kLpStages) & 1u)) sh.gave_up = 1;
+        ++taken;
       }
+#pragma unroll
+      for (int i = 0; i < kLpLoads; ++i)
+        x[i] = base + i * kLpThreads + tid < c1 ? *reinterpret_cast<const uint4 *>(st + (i * kLpThreads + tid) * 16) : En::none();
+      __syncthreads();  // the stage has been read by all, and so has the count of the list
+      if (tid == 0 && base < c1) issue();
       const float ex = (edge >= 0 && base == c0) ? to_f32(x0[edge]) : -INFINITY;
-      const float inner = En::largest(x), top = fmax3_nan(inner, ex, ex);
+      const float inner = En::largest_nan(x), top = fmax3_nan(inner, ex, ex);
       me.none |= !(top < INFINITY);
       // ---- sums, relative to the thread's own maximum
       if (top > me.m) {
@@ -253,17 +326,25 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas)
         w = __ffma2_rn(p, y, w);
       };
 #pragma unroll
-      for (int i = 0; i < kLpLoads; ++i) {
+      for (int i = 0; i < kLpLoads; ++i)
 #pragma unroll
         for (int e = 0; e < VE / 2; ++e) add(En::pair(x[i], e));
-        // ---- entries before the token
-        const int j0 = head + (base + i * kLpThreads + tid) * VE;
-        if (xt == -INFINITY && j0 + VE <= tok)  // nothing is below: every entry counts
-          me.before += base + i * kLpThreads + tid < c1 ? VE : 0;
-        else
-          me.before += En::above(x[i], j0 + VE <= tok ? xt_before : xt);
+      // ---- entries before the token
+      const int first = base + tid;
+      if (xt > -INFINITY) {
+        typename En::Count n{};
+#pragma unroll
+        for (int i = 0; i < kLpLoads; ++i) En::above(n, x[i], first + i * kLpThreads < tok_after ? xt_before : xt);
+        me.before += En::total(n);
+      } else {  // nothing is below: above it are the finite ones, and with a lower index every entry
+        for (int i = 0; i < kLpLoads; ++i) {
+          typename En::Count n{};
+          En::above(n, x[i], xt);
+          const int c = first + i * kLpThreads;
+          me.before += c < tok_after && c < c1 ? VE : En::total(n);
+        }
       }
-      if (tok_chunk >= base && tok_chunk < base + kLpThreads * kLpLoads && (tok_chunk - base) % kLpThreads == tid)
+      if (tok_chunk >= base && tok_chunk < base + kLpChunks && (tok_chunk - base) % kLpThreads == tid)
         for (int j = head + tok_chunk * VE; j < tok; ++j)  // of the token's own chunk, equal entries before it
           me.before += to_f32(x0[j]) == xt;
       if (edge >= 0 && base == c0) {
@@ -291,29 +372,30 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas)
         floor = sh.floor;
       }
       int over = 0;
-      if (top >= floor && top > -INFINITY) {  // few threads: which entries, then those one by one, read again
-        unsigned long long which = 0;
+      if (top >= floor && top > -INFINITY) {  // few threads: their few chunks with such an entry, read again
+        unsigned which = 0;
 #pragma unroll
-        for (int i = 0; i < kLpLoads; ++i)
-#pragma unroll
-          for (int e = 0; e < VE; ++e) {
-            const float2 v = En::pair(x[i], e / 2);
-            which |= static_cast<unsigned long long>((e % 2 ? v.y : v.x) >= floor) << (i * VE + e);
-          }
-        auto aside = [&](int j) {
-          const float v = to_f32(x0[j]);
-          if (v == -INFINITY) return;
-          const int at = atomicAdd(&sh.count, 1);
-          if (at < kLpList)
-            sh.list[at] = order_key(v, j);
+        for (int i = 0; i < kLpLoads; ++i) which |= static_cast<unsigned>(En::largest(x[i]) >= floor) << i;
+        auto aside = [&](float v, int j) {
+          if (!(v >= floor) || v == -INFINITY) return;
+          const int n = atomicAdd(&sh.count, 1);
+          if (n < kLpList)
+            sh.list[n] = order_key(v, j);
           else
             over = 1;
         };
         for (; which; which &= which - 1) {
-          const int bit = __ffsll(which) - 1, c = base + bit / VE * kLpThreads + tid;
-          if (c < c1) aside(head + c * VE + bit % VE);
+          const int c = first + (__ffs(which) - 1) * kLpThreads;
+          if (c >= c1) break;
+          const uint4 again = __ldg(reinterpret_cast<const uint4 *>(x0 + head) + c);
+#pragma unroll
+          for (int e = 0; e < VE / 2; ++e) {
+            const float2 v = En::pair(again, e);
+            aside(v.x, head + c * VE + 2 * e);
+            aside(v.y, head + c * VE + 2 * e + 1);
+          }
         }
-        if (edge >= 0 && base == c0 && ex >= floor) aside(edge);
+        if (edge >= 0 && base == c0) aside(ex, edge);
       }
       over = __syncthreads_or(over);
       const int n = sh.count;
@@ -327,7 +409,7 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas)
             if (key < last && key > b) b = key;
           };
           for (int i = tid; i < kLpList; i += kLpThreads) see(sh.list[i]);
-          const int e1 = head + min(base + kLpThreads * kLpLoads, c1) * VE;
+          const int e1 = head + min(base + kLpChunks, c1) * VE;
           for (int j = head + base * VE + tid; j < e1; j += kLpThreads) {
             const float v = to_f32(x0[j]);
             if (v > -INFINITY) see(order_key(v, j));
@@ -348,16 +430,17 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas)
       } else if (n > kLpCut) {
         put_in_order(sh.list, n, sh.best, K);
       } else {
-        __syncthreads();  // the count has been read by all
         continue;
       }
       // the best K are the list now
       if (tid < K) sh.list[tid] = sh.best[tid];
       if (tid == 0) sh.count = K;
       if (sh.best[K - 1] != 0) floor = fmaxf(floor, key_value(sh.best[K - 1]));
-      __syncthreads();
     }
-    if (K > 0) put_in_order(sh.list, sh.count, sh.best, K);
+    if (K > 0) {
+      __syncthreads();
+      put_in_order(sh.list, sh.count, sh.best, K);
+    }
     // ---- this CTA's part
     for (int o = 16; o; o >>= 1) {
       RowPart y;
@@ -430,18 +513,26 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas)
     else
       __syncthreads();
   }
+  if (tid == 0 && sh.gave_up) atomicOr(&hdr->err[0], 0x8u);  // (2 s after the call's bits were written)
 }
 
 template <typename Tin>
 cudaError_t logprobs_one(const LogprobArgs &a) {
-  // CTAs a row: as many as the row fills, up to 8, for few rows; with many rows fewer and longer parts,
-  // as long as about eight waves of CTAs are left to even out the ends.
+  // CTAs a row: as many as the row has work for, up to 8, for few rows; with many rows fewer with longer
+  // parts, as long as five rows are left for a cluster to even out the ends.
+  const int slots = kLpCtas * current_sm_count();
   int C = 1;
   while (C < kLpMaxCluster && a.V > C * kLpThreads * kLpLoads * 2) C *= 2;
-  while (C > 1 && static_cast<int64_t>(a.R) * (C / 2) >= 8LL * kLpCtas * current_sm_count()) C /= 2;
-  return launch_pdl_cluster(logprobs_kernel<Tin>, dim3(C, std::min(a.R, 65535)), dim3(kLpThreads), dim3(C), 0, a.stream,
-                            static_cast<const Tin *>(a.logits), a.row_stride, a.tokens, a.R, a.V, a.K, a.logprob,
-                            a.entropy, a.rank, a.top_ids, a.top_logprobs, static_cast<WsHeader *>(a.ws));
+  while (C > 1 && static_cast<int64_t>(a.R) * (C / 2) >= 5LL * slots) C /= 2;
+  auto kern = logprobs_kernel<Tin>;
+  constexpr int smem = kLpStages * kLpStageBytes;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  e = cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
+  if (e != cudaSuccess) return e;
+  return launch_pdl_cluster(kern, dim3(C, std::min(a.R, std::max(1, slots / C))), dim3(kLpThreads), dim3(C), smem,
+                            a.stream, static_cast<const Tin *>(a.logits), a.row_stride, a.tokens, a.R, a.V, a.K,
+                            a.logprob, a.entropy, a.rank, a.top_ids, a.top_logprobs, static_cast<WsHeader *>(a.ws));
 }
 
 }  // namespace

@@ -10,8 +10,8 @@
 // are equal and ties need no rule of their own.
 //
 // Bound by HBM.  A cluster of up to 8 CTAs shares a row, and the clusters that fit the GPU
-// walk the rows.  Blocks of 32 KB come by bulk copies into two stages of shared memory,
-// the next two on their way whatever the CTA is at, across rows as well.  Each thread
+// walk the rows that have a token.  Blocks of 32 KB come by bulk copies into two stages of
+// shared memory, one on its way while one is worked on, across rows as well.  Each thread
 // takes 128 bytes of a block, folds them into its own running sums (relative to its
 // own maximum), counts those before the token, and puts aside
 // those that can be alternatives: of the 64 groups of 4 threads, each with its largest
@@ -32,6 +32,7 @@ constexpr int kLpCtas = 3;                        // CTAs of an SM
 constexpr int kLpLoads = 8;                       // 16-byte chunks of a thread in a block
 constexpr int kLpChunks = kLpThreads * kLpLoads;  // chunks of a block
 constexpr int kLpStages = 2;
+constexpr int kLpRows = 4;                        // rows listed ahead
 constexpr int kLpStageBytes = kLpChunks * 16;
 constexpr int kLpGroups = 64;                     // groups of threads, the candidates for the bound
 constexpr int kLpList = 512;                      // entries put aside
@@ -74,6 +75,7 @@ struct LpShared {
   float group[kLpGroups];
   float floor;     // no alternative is below this value
   int count;
+  int64_t found[kLpRows];    // rows of this cluster that are to come
   uint64_t full[kLpStages];  // mbarriers: a block has landed
   int gave_up;
 };
@@ -185,6 +187,17 @@ __device__ __forceinline__ void fold(RowPart &a, const RowPart &b) {
   a.m = m;
 }
 
+// The parts of a warp's lanes, in every lane.
+__device__ __forceinline__ void warp_fold(RowPart &a) {
+  const float m = warp_max_xor(a.m, 1, 16);
+  const float d = a.m == -INFINITY ? -300.f : (a.m - m) * kLog2e, e = ex2(d);  // nothing: sums of 0
+  a.w = warp_sum_xor(e > 0.f ? (a.w + a.z * d) * e : 0.f, 1, 16);
+  a.z = warp_sum_xor(a.z * e, 1, 16);
+  a.m = m;
+  a.before = __reduce_add_sync(0xffffffffu, a.before);
+  a.none = __any_sync(0xffffffffu, a.none);
+}
+
 // The n keys of `from` (room for one more) in descending order into `to`, at most K of them, which are
 // cleared first: each key's place is the number of larger ones.  Every thread takes part; begins and ends
 // with a barrier.
@@ -235,43 +248,73 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas)
     sh.gave_up = 0;
   }
   __syncthreads();
-  // thread 0 is two blocks ahead: its place in the sequence of rows with a token and their blocks
-  int64_t ahead = blockIdx.y;
-  int ahead_block = 0, issued = 0;
-  auto issue = [&] {
-    for (; ahead < R; ahead += gridDim.y, ahead_block = 0) {
-      const int t = tokens[ahead];
-      if (t < 0 || t >= V) continue;
-      const RowPlace<Tin> p(logits + ahead * stride, V, C, part);
-      if (ahead_block >= p.blocks()) continue;
-      const int c = p.c0 + ahead_block * kLpChunks;
-      const uint32_t bytes = 16u * min(kLpChunks, p.c1 - c);
-      const int st = issued++ % kLpStages;
-      mbar_arrive_expect_tx(&sh.full[st], bytes);
-      bulk_load(stages + st * kLpStageBytes, reinterpret_cast<const uint4 *>(p.x + p.head) + c, bytes, &sh.full[st]);
-      ++ahead_block;
-      return;
+  // rows without a token
+  for (int64_t i = (static_cast<int64_t>(blockIdx.y) * C + part) * kLpThreads + tid; i < R;
+       i += static_cast<int64_t>(gridDim.y) * C * kLpThreads) {
+    const int t = tokens[i];
+    if (t >= 0 && t < V) continue;
+    logprob[i] = 0.f;
+    entropy[i] = 0.f;
+    rank[i] = -1;
+    for (int k = 0; k < K; ++k) {
+      top_ids[i * K + k] = -1;
+      top_lp[i * K + k] = -INFINITY;
     }
+  }
+  // The rows with a token go round the clusters: cluster y has those whose number among them is y modulo
+  // gridDim.y.  Warp 0 walks them ahead of the others and asks for their blocks; found[] holds the rows
+  // it has come to and that are not done with.
+  int64_t scan = 0, ahead = -1;    // rows before `scan` have been walked; the row whose blocks are asked for
+  int wanted = blockIdx.y;         // number, counted from `scan`, of this cluster's next row with a token
+  int ahead_block = 0, issued = 0, taken = 0;  // blocks asked for and used
+  int listed = 0, done = 0;        // rows found and done with
+  auto next_row = [&]() -> int64_t {
+    while (scan < R) {
+      const int t = scan + lane < R ? tokens[scan + lane] : -1;
+      const unsigned live = __ballot_sync(0xffffffffu, t >= 0 && t < V);
+      const unsigned it = __ballot_sync(0xffffffffu, (live >> lane & 1u) && __popc(live & ((1u << lane) - 1u)) == wanted);
+      if (it) {
+        const int64_t row = scan + __ffs(it) - 1;
+        scan = row + 1;
+        wanted = gridDim.y - 1;
+        return row;
+      }
+      wanted -= __popc(live);
+      scan += 32;
+    }
+    return R;
   };
-  if (tid == 0)
-    for (int i = 0; i < kLpStages; ++i) issue();
-  int taken = 0;  // blocks used
-  for (int64_t row = blockIdx.y; row < R; row += gridDim.y) {
-    const int tok = tokens[row];
-    if (tok < 0 || tok >= V) {  // no token (the whole cluster sees that)
-      if (part == 0) {
-        if (tid == 0) {
-          logprob[row] = 0.f;
-          entropy[row] = 0.f;
-          rank[row] = -1;
-        }
-        if (tid < K) {
-          top_ids[row * K + tid] = -1;
-          top_lp[row * K + tid] = -INFINITY;
+  auto fill = [&] {  // warp 0: blocks for the stages that are free
+    while (issued - taken < kLpStages) {
+      if (ahead >= 0) {
+        if (ahead == R) return;
+        const RowPlace<Tin> p(logits + ahead * stride, V, C, part);
+        if (ahead_block < p.blocks()) {
+          if (lane == 0) {
+            const int c = p.c0 + ahead_block * kLpChunks;
+            const uint32_t bytes = 16u * min(kLpChunks, p.c1 - c);
+            const int st = issued % kLpStages;
+            mbar_arrive_expect_tx(&sh.full[st], bytes);
+            bulk_load(stages + st * kLpStageBytes, reinterpret_cast<const uint4 *>(p.x + p.head) + c, bytes, &sh.full[st]);
+          }
+          ++issued;
+          ++ahead_block;
+          continue;
         }
       }
-      continue;
+      if (listed - done == kLpRows) return;  // parts without blocks ask for none: rows are listed all the same
+      ahead = next_row();
+      ahead_block = 0;
+      if (lane == 0) sh.found[listed % kLpRows] = ahead;
+      ++listed;
     }
+  };
+  if (warp == 0) fill();
+  for (;; ++done) {
+    __syncthreads();
+    const int64_t row = sh.found[done % kLpRows];
+    if (row == R) break;  // (the whole cluster comes to the same end)
+    const int tok = tokens[row];
     const RowPlace<Tin> at(logits + row * stride, V, C, part);
     const Tin *x0 = at.x;
     const int head = at.head, tail = at.tail, c0 = at.c0, c1 = at.c1;
@@ -297,13 +340,10 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas)
       const unsigned char *st = stages + taken % kLpStages * kLpStageBytes;
       if (base < c1) {
         if (!mbar_wait(&sh.full[taken % kLpStages], (taken / kLpStages) & 1u)) sh.gave_up = 1;
-        ++taken;
       }
 #pragma unroll
       for (int i = 0; i < kLpLoads; ++i)
         x[i] = base + i * kLpThreads + tid < c1 ? *reinterpret_cast<const uint4 *>(st + (i * kLpThreads + tid) * 16) : En::none();
-      __syncthreads();  // the stage has been read by all, and so has the count of the list
-      if (tid == 0 && base < c1) issue();
       const float ex = (edge >= 0 && base == c0) ? to_f32(x0[edge]) : -INFINITY;
       const float inner = En::largest_nan(x), top = fmax3_nan(inner, ex, ex);
       me.none |= !(top < INFINITY);
@@ -353,9 +393,8 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas)
       }
       me.z += z.x + z.y;
       me.w += w.x + w.y;
-      if (K == 0) continue;
       // ---- alternatives
-      if (base == c0) {  // the bound that the first block gives
+      if (K > 0 && base == c0) {  // the bound that the first block gives
         float g = top;
 #pragma unroll
         for (int o = 1; o < kPerGroup; o <<= 1) g = fmaxf(g, __shfl_xor_sync(0xffffffffu, g, o));
@@ -371,35 +410,42 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas)
         __syncthreads();
         floor = sh.floor;
       }
-      int over = 0;
-      if (top >= floor && top > -INFINITY) {  // few threads: their few chunks with such an entry, read again
+      int grown = 0;
+      if (K > 0 && top >= floor && top > -INFINITY) {  // few threads: their few chunks with such an entry
         unsigned which = 0;
 #pragma unroll
         for (int i = 0; i < kLpLoads; ++i) which |= static_cast<unsigned>(En::largest(x[i]) >= floor) << i;
         auto aside = [&](float v, int j) {
           if (!(v >= floor) || v == -INFINITY) return;
           const int n = atomicAdd(&sh.count, 1);
-          if (n < kLpList)
-            sh.list[n] = order_key(v, j);
-          else
-            over = 1;
+          if (n < kLpList) sh.list[n] = order_key(v, j);
+          grown |= n >= kLpCut;
         };
         for (; which; which &= which - 1) {
           const int c = first + (__ffs(which) - 1) * kLpThreads;
           if (c >= c1) break;
-          const uint4 again = __ldg(reinterpret_cast<const uint4 *>(x0 + head) + c);
+          const Tin *chunk = reinterpret_cast<const Tin *>(st + (c - base) * 16);
+          const uint4 again = *reinterpret_cast<const uint4 *>(chunk);
+          unsigned those = 0;
 #pragma unroll
-          for (int e = 0; e < VE / 2; ++e) {
-            const float2 v = En::pair(again, e);
-            aside(v.x, head + c * VE + 2 * e);
-            aside(v.y, head + c * VE + 2 * e + 1);
+          for (int e = 0; e < VE; ++e) {
+            const float2 v = En::pair(again, e / 2);
+            those |= static_cast<unsigned>((e % 2 ? v.y : v.x) >= floor) << e;
+          }
+          for (; those; those &= those - 1) {  // mostly one
+            const int e = __ffs(those) - 1;
+            aside(to_f32(chunk[e]), head + c * VE + e);
           }
         }
         if (edge >= 0 && base == c0) aside(ex, edge);
       }
-      over = __syncthreads_or(over);
-      const int n = sh.count;
-      if (over) {
+      grown = __syncthreads_or(grown);  // this block's stage and list are done with
+      if (base < c1) {
+        ++taken;
+        if (warp == 0) fill();
+      }
+      if (!grown) continue;
+      if (sh.count > kLpList) {
         // more than the list holds: the largest key below the last one, K times, of this block and of what
         // the list had before it (entries of this block that are in the list count once: keys are unique)
         unsigned long long last = ~0ull;
@@ -427,48 +473,29 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas)
           last = b;
           __syncthreads();
         }
-      } else if (n > kLpCut) {
-        put_in_order(sh.list, n, sh.best, K);
       } else {
-        continue;
+        put_in_order(sh.list, sh.count, sh.best, K);
       }
       // the best K are the list now
       if (tid < K) sh.list[tid] = sh.best[tid];
       if (tid == 0) sh.count = K;
       if (sh.best[K - 1] != 0) floor = fmaxf(floor, key_value(sh.best[K - 1]));
-    }
-    if (K > 0) {
       __syncthreads();
-      put_in_order(sh.list, sh.count, sh.best, K);
     }
+    if (K > 0) put_in_order(sh.list, sh.count, sh.best, K);
     // ---- this CTA's part
-    for (int o = 16; o; o >>= 1) {
-      RowPart y;
-      y.m = __shfl_xor_sync(0xffffffffu, me.m, o);
-      y.z = __shfl_xor_sync(0xffffffffu, me.z, o);
-      y.w = __shfl_xor_sync(0xffffffffu, me.w, o);
-      fold(me, y);
-    }
-    me.before = __reduce_add_sync(0xffffffffu, me.before);
-    me.none = __any_sync(0xffffffffu, me.none);
+    warp_fold(me);
     if (lane == 0) sh.warp[warp] = me;
     __syncthreads();
     if (warp == 0) {
-      me = sh.warp[lane & (kLpThreads / 32 - 1)];
-      if (lane >= kLpThreads / 32) {
+      if (lane < kLpThreads / 32) {
+        me = sh.warp[lane];
+      } else {
         me.m = -INFINITY;
         me.z = me.w = 0.f;
         me.before = me.none = 0;
       }
-      for (int o = 16; o; o >>= 1) {
-        RowPart y;
-        y.m = __shfl_xor_sync(0xffffffffu, me.m, o);
-        y.z = __shfl_xor_sync(0xffffffffu, me.z, o);
-        y.w = __shfl_xor_sync(0xffffffffu, me.w, o);
-        fold(me, y);
-      }
-      me.before = __reduce_add_sync(0xffffffffu, me.before);
-      me.none = __any_sync(0xffffffffu, me.none);
+      warp_fold(me);
       if (lane < 8) {  // to the first CTA: the part as eight words
         const float v = lane == 0 ? me.m : lane == 1 ? me.z : lane == 2 ? me.w : __int_as_float(lane == 3 ? me.before : lane == 4 ? me.none : 0);
         st_cluster_f(reinterpret_cast<float *>(&sh.part[part]) + lane, 0, v);
@@ -507,23 +534,24 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas)
         }
       }
     }
-    // the next row's parts come after this one's have been read
-    if (C > 1)
-      cluster_sync_all();
-    else
-      __syncthreads();
+    if (warp == 0) {
+      ++done;
+      fill();  // a row without blocks of its own has asked for none
+      --done;
+    }
+    if (C > 1) cluster_sync_all();  // the next row's parts come after this one's have been read
   }
   if (tid == 0 && sh.gave_up) atomicOr(&hdr->err[0], 0x8u);  // (2 s after the call's bits were written)
 }
 
 template <typename Tin>
 cudaError_t logprobs_one(const LogprobArgs &a) {
-  // CTAs a row: as many as the row has work for, up to 8, for few rows; with many rows fewer with longer
-  // parts, as long as five rows are left for a cluster to even out the ends.
+  // CTAs a row: as many as the row has work for, up to 8, as long as there are not rows enough to go
+  // round without: meeting costs a cluster about 3 us a row (640 rows of 128256 float32: 86 us by fours,
+  // 48 us by one; 4 rows: 10.7 us by eights, 30 us by one).
   const int slots = kLpCtas * current_sm_count();
   int C = 1;
-  while (C < kLpMaxCluster && a.V > C * kLpThreads * kLpLoads * 2) C *= 2;
-  while (C > 1 && static_cast<int64_t>(a.R) * (C / 2) >= 5LL * slots) C /= 2;
+  while (C < kLpMaxCluster && a.V > C * kLpThreads * kLpLoads * 2 && static_cast<int64_t>(a.R) * C < slots) C *= 2;
   auto kern = logprobs_kernel<Tin>;
   constexpr int smem = kLpStages * kLpStageBytes;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);

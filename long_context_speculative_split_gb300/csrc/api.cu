@@ -130,12 +130,15 @@ bool pdl_enabled() { return g_pdl.load(std::memory_order_relaxed) != 0; }
 void record_error(const char *msg) { g_last_error = msg; }
 
 int current_sm_count() {
+  static std::atomic<int> known[64];  // by device; 0: not asked yet
   int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) == cudaSuccess && dev < 64 && (n = known[dev].load(std::memory_order_relaxed)) > 0) return n;
   if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
       n <= 0) {
     cudaGetLastError();  // clear the sticky-free error of a missing device
     return 152;
   }
+  if (dev < 64) known[dev].store(n, std::memory_order_relaxed);
   return n;
 }
 
@@ -517,6 +520,8 @@ mgd_status mgd_prefix_attn(const void *q, const void *k_prefix, const void *v_pr
   if (ws_bytes < plan.ws_bytes) return fail(MGD_ERR_WORKSPACE, "workspace %zu < %zu bytes", ws_bytes, plan.ws_bytes);
   if (static_cast<int64_t>(plan.g.RT) * Hkv * ((prefix_cap + plan.g.key_tile - 1) / plan.g.key_tile) > INT32_MAX)
     return fail(MGD_ERR_UNSUPPORTED, "too many rows and prefix keys for one call");
+  if (in_f32 && static_cast<int64_t>(B) * Hkv * plan.chunks.row_tiles * plan.chunks.count + plan.grid > INT32_MAX)
+    return fail(MGD_ERR_UNSUPPORTED, "too many rows and own keys for one call");
   PrefixArgs a;
   a.q = q;
   a.k = k_prefix;
@@ -530,15 +535,6 @@ mgd_status mgd_prefix_attn(const void *q, const void *k_prefix, const void *v_pr
   a.ws = ws;
   a.stream = static_cast<cudaStream_t>(stream);
   unsigned char *w = static_cast<unsigned char *>(ws);
-  if (in_f32) {
-    // this attention clears the header ahead of its launch, so the prefix kernel raises its bits after it
-    s = run_attention(q, k, v, kv_len, B, T, Hq, Hkv, D, kv_cap, kv_batch_stride, kv_head_stride, sm_scale, in_dtype,
-                      w + plan.off_own_o, MGD_F32, reinterpret_cast<float *>(w + plan.off_own_l), ws, ws_bytes, stream);
-    if (s != MGD_OK) return s;
-    cudaError_t e = launch_prefix_simt(plan, a);
-    if (e == cudaSuccess) e = launch_prefix_merge(plan, a);
-    return e == cudaSuccess ? ok() : cuda_fail(e, "prefix attention (float32) launch");
-  }
   AttnArgs o;
   o.q = q;
   o.k = k;
@@ -552,6 +548,11 @@ mgd_status mgd_prefix_attn(const void *q, const void *k_prefix, const void *v_pr
   o.lse = reinterpret_cast<float *>(w + plan.off_own_l);
   o.ws = ws;
   o.stream = a.stream;
+  if (in_f32) {
+    cudaError_t e = launch_prefix_simt(plan, a, o);
+    if (e == cudaSuccess) e = launch_prefix_merge(plan, a, kv_len);
+    return e == cudaSuccess ? ok() : cuda_fail(e, "prefix attention (float32) launch");
+  }
   // each CTA of a pair loads half of a key group's keys of K and half of a key tile's columns of V
   const int64_t all = prefix_head_stride * Hkv;
   const int G = Hq / Hkv;
@@ -567,7 +568,7 @@ mgd_status mgd_prefix_attn(const void *q, const void *k_prefix, const void *v_pr
   cudaError_t e = clear_attention_tickets(plan.own, ws, a.stream);
   if (e == cudaSuccess) e = launch_prefix_tc05(plan, a, pk, pv, q_tma ? &pq : nullptr);
   if (e == cudaSuccess) e = launch_attention_beside(plan.own, o, km, vm);
-  if (e == cudaSuccess) e = launch_prefix_merge(plan, a);
+  if (e == cudaSuccess) e = launch_prefix_merge(plan, a, kv_len);
   return e == cudaSuccess ? ok() : cuda_fail(e, "prefix attention launch");
 }
 

@@ -636,9 +636,7 @@ cudaError_t launch_one(const AttnPlan &pl, const AttnArgs &a, const CUtensorMap 
   constexpr int MINB = (NT <= 3) ? 2 : 1;
   auto kern = attn_tc_kernel<D, NT, MINB, kBeside>;
   const int smem = Layout<D, NT>::alloc;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (e != cudaSuccess) return e;
-  e = cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
+  cudaError_t e = want_shared_memory<attn_tc_kernel<D, NT, MINB, kBeside>>(smem);
   if (e != cudaSuccess) return e;
   KParams kp;
   kp.T = pl.T;

@@ -116,11 +116,17 @@ struct PrefixGeom {
   int slot_rows;  // rows kept per partial result, min(tile_rows, R)
   int prefix_cap;
 };
+// float32: the own caches in chunks of `keys`, one partial result for each (sequence, KV head, row tile) and
+// chunk; count == 0: one result a row.
+struct OwnChunks {
+  int count, keys, row_tiles, slot_rows, cap;
+};
 struct PrefixPlan {
   PrefixGeom g;
-  AttnPlan own;     // attention over each sequence's own cache
+  AttnPlan own;     // bf16: attention over each sequence's own cache
+  OwnChunks chunks;
   int own_cap, grid;  // grid: CTAs of the float32 prefix kernel, clusters of the bf16 one
-  size_t off_own_o, off_own_l;    // float [B][T][Hq][D], [B][T][Hq]
+  size_t off_own_o, off_own_l;    // float [B][T][Hq][D], [B][T][Hq], or the chunks'
   size_t off_part_o, off_part_l;  // float [slots][slot_rows][D], [slots][slot_rows]
   size_t ws_bytes;
 };
@@ -145,8 +151,9 @@ struct PrefixArgs {
 int prefix_tc05_clusters(int D, int most);  // clusters of the bf16 kernel that run at once on the current device
 cudaError_t launch_prefix_tc05(const PrefixPlan &p, const PrefixArgs &a, const CUtensorMap &kmap,
                                const CUtensorMap &vmap, const CUtensorMap *qmap);  // bf16; qmap nullable
-cudaError_t launch_prefix_simt(const PrefixPlan &p, const PrefixArgs &a);                           // float32
-cudaError_t launch_prefix_merge(const PrefixPlan &p, const PrefixArgs &a);
+// float32, over the prefix and the own caches
+cudaError_t launch_prefix_simt(const PrefixPlan &p, const PrefixArgs &a, const AttnArgs &own);
+cudaError_t launch_prefix_merge(const PrefixPlan &p, const PrefixArgs &a, const int32_t *kv_len);
 // The bf16 attention over the own caches, launched right after the prefix kernel: it runs beside that
 // one on the SMs that are left, and its results are complete when both are.
 cudaError_t launch_attention_beside(const AttnPlan &p, const AttnArgs &a, const CUtensorMap &kmap,

@@ -36,7 +36,7 @@ constexpr int kLpRows = 4;                        // rows listed ahead
 constexpr int kLpStageBytes = kLpChunks * 16;
 constexpr int kLpGroups = 64;                     // groups of threads, the candidates for the bound
 constexpr int kLpList = 512;                      // entries put aside
-constexpr int kLpCut = 96;                        // a list longer than this is cut to the best K
+constexpr int kLpCut = 56;                        // a list longer than this is cut to the best K
 constexpr int kLpMaxK = 32;                       // kLpGroups bounds it
 constexpr int kLpMaxCluster = 8;
 constexpr float kLog2e = 1.4426950408889634f;
@@ -552,13 +552,10 @@ cudaError_t logprobs_one(const LogprobArgs &a) {
   const int slots = kLpCtas * current_sm_count();
   int C = 1;
   while (C < kLpMaxCluster && a.V > C * kLpThreads * kLpLoads * 2 && static_cast<int64_t>(a.R) * C < slots) C *= 2;
-  auto kern = logprobs_kernel<Tin>;
   constexpr int smem = kLpStages * kLpStageBytes;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  cudaError_t e = want_shared_memory<logprobs_kernel<Tin>>(smem);
   if (e != cudaSuccess) return e;
-  e = cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
-  if (e != cudaSuccess) return e;
-  return launch_pdl_cluster(kern, dim3(C, std::min(a.R, std::max(1, slots / C))), dim3(kLpThreads), dim3(C), smem,
+  return launch_pdl_cluster(logprobs_kernel<Tin>, dim3(C, std::min(a.R, std::max(1, slots / C))), dim3(kLpThreads), dim3(C), smem,
                             a.stream, static_cast<const Tin *>(a.logits), a.row_stride, a.tokens, a.R, a.V, a.K,
                             a.logprob, a.entropy, a.rank, a.top_ids, a.top_logprobs, static_cast<WsHeader *>(a.ws));
 }

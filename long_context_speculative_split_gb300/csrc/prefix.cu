@@ -5,8 +5,8 @@
 // With s_j = scale <q, k_j>, the softmax over prefix and own keys splits exactly:
 //   (O_P, l_P), (O_b, l_b) = the two parts' outputs and log-sum-exps
 //   l = log(e^{l_P} + e^{l_b}),  O = e^{l_P - l} O_P + e^{l_b - l} O_b.
-// The own part is the verify attention kernel with a float32 output; the prefix part has
-// B * T * G query rows a KV head instead of T * G, which turns the one
+// The own part is the verify attention kernel with a float32 output (float32 inputs: the
+// tiles below); the prefix part has B * T * G query rows a KV head instead of T * G, which turns the one
 // read of the prefix into a matrix product.
 #include <algorithm>
 
@@ -20,7 +20,7 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
 // ---------------------------------------------------------------- CUDA cores
-// Tiles of 64 rows x 64 keys, float32 throughout: 256 threads as 16 x 16, each
+// Tiles of 64 rows x 64 keys, float32 throughout (prefix and own caches alike): 256 threads as 16 x 16, each
 // with 4 x 4 scores and 4 x D/16 outputs in registers, K and V tiles in shared
 // memory, the running maximum and sum of a row held by the 16 threads that share
 // it.  It serves float32 inputs (the tensor cores have no float32 form).
@@ -36,146 +36,188 @@ struct SimtLayout {
   static constexpr int bytes = (off_p + kSRows * kPStride) * 4;
 };
 
-__device__ __forceinline__ float4 load4(const float *p) { return *reinterpret_cast<const float4 *>(p); }
-
-template <int D>
-__global__ void __launch_bounds__(kSThreads)
-    prefix_simt_kernel(const float *__restrict__ q, const float *__restrict__ k, const float *__restrict__ v,
-                       const int32_t *__restrict__ prefix_len, int64_t head_stride, float sl2, PrefixGeom g,
-                       float *__restrict__ part_o, float *__restrict__ part_l, WsHeader *hdr) {
-  pdl_launch_dependents();
-  pdl_wait();
+// The 64 query rows `q_row(r)` (null: no such row) over keys [key0, key1) of one KV head, row r only over
+// those below `limit(r)`: normalised outputs and log-sum-exps of the first `rows` of them to po, pl.
+template <int D, typename QRow, typename Limit>
+__device__ __forceinline__ void simt_rows(float *sm, const float *kb, const float *vb, int key0, int key1,
+                                          float sl2, const QRow &q_row, const Limit &limit, int rows, float *po,
+                                          float *pl) {
   using Lay = SimtLayout<D>;
   constexpr int NC = D / 64;  // float4 output columns a thread holds, 64 apart
-  extern __shared__ float sm[];
   float *sq = sm, *sk = sm + Lay::off_k, *sv = sm + Lay::off_v, *sp = sm + Lay::off_p;
+  const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
+  const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
+  __syncthreads();
+  for (int i = threadIdx.x; i < kSRows * (D / 4); i += kSThreads) {
+    const int r = i / (D / 4), d = 4 * (i % (D / 4));
+    const float *qr = q_row(r);
+    *reinterpret_cast<float4 *>(sq + r * Lay::kStride + d) = qr ? *reinterpret_cast<const float4 *>(qr + d) : zero;
+  }
+  float m[4], l[4], acc[4][4 * NC];
+  int lim[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    m[i] = -INFINITY;
+    l[i] = 0.f;
+    lim[i] = limit(4 * ty + i);
+#pragma unroll
+    for (int e = 0; e < 4 * NC; ++e) acc[i][e] = 0.f;
+  }
+  for (int base = key0; base < key1; base += kSKeys) {
+    __syncthreads();  // the tile before has been read
+    for (int i = threadIdx.x; i < kSKeys * (D / 4); i += kSThreads) {
+      const int r = i / (D / 4), d = 4 * (i % (D / 4));
+      const bool in = base + r < key1;  // rows past the end hold anything
+      const int64_t off = static_cast<int64_t>(base + r) * D + d;
+      *reinterpret_cast<float4 *>(sk + r * Lay::kStride + d) = in ? *reinterpret_cast<const float4 *>(kb + off) : zero;
+      *reinterpret_cast<float4 *>(sv + r * Lay::kStride + d) = in ? *reinterpret_cast<const float4 *>(vb + off) : zero;
+    }
+    __syncthreads();
+    float s[4][4] = {};
+    for (int d = 0; d < D; d += 4) {
+      float4 a[4], b[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) a[i] = *reinterpret_cast<const float4 *>(sq + (4 * ty + i) * Lay::kStride + d);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) b[j] = *reinterpret_cast<const float4 *>(sk + (tx + 16 * j) * Lay::kStride + d);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          s[i][j] = fmaf(a[i].x, b[j].x, s[i][j]);
+          s[i][j] = fmaf(a[i].y, b[j].y, s[i][j]);
+          s[i][j] = fmaf(a[i].z, b[j].z, s[i][j]);
+          s[i][j] = fmaf(a[i].w, b[j].w, s[i][j]);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float mx = -INFINITY;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        s[i][j] = base + tx + 16 * j < min(lim[i], key1) ? s[i][j] * sl2 : -INFINITY;
+        mx = fmaxf(mx, s[i][j]);
+      }
+      mx = fmaxf(m[i], warp_max_xor(mx, 1, 8));
+      const float mu = (mx == -INFINITY) ? 0.f : mx;
+      const float alpha = exp2f(m[i] - mu);
+      float sum = 0.f;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float e = exp2f(s[i][j] - mu);
+        sum += e;
+        sp[(4 * ty + i) * Lay::kPStride + tx + 16 * j] = e;
+      }
+      l[i] = l[i] * alpha + warp_sum_xor(sum, 1, 8);
+      m[i] = mx;
+#pragma unroll
+      for (int e = 0; e < 4 * NC; ++e) acc[i][e] *= alpha;
+    }
+    __syncwarp();  // a row's 64 probabilities come from the 16 threads of its own half-warp
+    for (int j = 0; j < kSKeys; j += 4) {
+      float4 pr[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) pr[i] = *reinterpret_cast<const float4 *>(sp + (4 * ty + i) * Lay::kPStride + j);
+#pragma unroll
+      for (int jj = 0; jj < 4; ++jj)
+#pragma unroll
+        for (int cc = 0; cc < NC; ++cc) {
+          const float4 vv = *reinterpret_cast<const float4 *>(sv + (j + jj) * Lay::kStride + 64 * cc + 4 * tx);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float pe = jj == 0 ? pr[i].x : jj == 1 ? pr[i].y : jj == 2 ? pr[i].z : pr[i].w;
+            acc[i][4 * cc] = fmaf(pe, vv.x, acc[i][4 * cc]);
+            acc[i][4 * cc + 1] = fmaf(pe, vv.y, acc[i][4 * cc + 1]);
+            acc[i][4 * cc + 2] = fmaf(pe, vv.z, acc[i][4 * cc + 2]);
+            acc[i][4 * cc + 3] = fmaf(pe, vv.w, acc[i][4 * cc + 3]);
+          }
+        }
+    }
+    __syncwarp();
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int r = 4 * ty + i;
+    if (r >= rows) continue;
+    const float inv = l[i] > 0.f ? 1.f / l[i] : 0.f;
+#pragma unroll
+    for (int cc = 0; cc < NC; ++cc)
+      *reinterpret_cast<float4 *>(po + r * D + 64 * cc + 4 * tx) =
+          make_float4(acc[i][4 * cc] * inv, acc[i][4 * cc + 1] * inv, acc[i][4 * cc + 2] * inv, acc[i][4 * cc + 3] * inv);
+    if (tx == 0) pl[r] = l[i] > 0.f ? (m[i] + log2f(l[i])) * kLn2 : -INFINITY;
+  }
+}
+
+// The first n_prefix CTAs take their parts of the prefix's line of steps; the others one (sequence, KV head,
+// 64 of its T * G rows) and chunk of own keys each.
+struct SimtParams {
+  PrefixGeom g;
+  OwnChunks own;
+  int n_prefix;
+  float sl2;
+  int64_t prefix_hstride, own_bstride, own_hstride;
+};
+template <int D>
+__global__ void __launch_bounds__(kSThreads)
+    prefix_simt_kernel(const float *__restrict__ q, const float *__restrict__ k_prefix,
+                       const float *__restrict__ v_prefix, const int32_t *__restrict__ prefix_len,
+                       const float *__restrict__ k_own, const float *__restrict__ v_own,
+                       const int32_t *__restrict__ kv_len, float *__restrict__ part_o, float *__restrict__ part_l,
+                       float *__restrict__ own_o, float *__restrict__ own_l, WsHeader *hdr, SimtParams p) {
+  pdl_launch_dependents();
+  pdl_wait();
+  extern __shared__ float sm[];
+  const PrefixGeom &g = p.g;
+  const OwnChunks &own = p.own;
   const int plen = prefix_len[0];
-  if (plen < 0 || plen > g.prefix_cap) {
-    if (blockIdx.x == 0 && threadIdx.x == 0) raise_error_sr(hdr, 0x1u);
+  const bool valid = plen >= 0 && plen <= g.prefix_cap;
+  if (blockIdx.x == 0) {
+    // one CTA looks at every length and writes the call's error bits
+    int bad = !valid;
+    for (int i = threadIdx.x; i < g.B; i += kSThreads) bad |= kv_len[i] < g.T || kv_len[i] > own.cap;
+    bad = __syncthreads_or(bad);
+    if (threadIdx.x == 0) {
+      hdr->err[0] = bad ? 0x1u : 0u;
+      hdr->err[1] = 0u;
+    }
+  }
+  if (static_cast<int>(blockIdx.x) < p.n_prefix) {
+    const PrefixLine w = prefix_line(g, valid ? plen : 0, p.n_prefix);
+    const int c = blockIdx.x;
+    if (c >= w.n) return;
+    const int x1 = prefix_cta_begin(w, c + 1);
+    for (int x = prefix_cta_begin(w, c); x < x1;) {
+      const int h = x / w.head;
+      const int rt = min((x - h * w.head) / w.nt, g.RT - 1);
+      const int begin = prefix_pair_begin(w, h, rt);
+      const int end = min(x1, begin + prefix_pair_steps(g, w, rt));
+      const int row0 = rt * kSRows;
+      const int64_t slot = static_cast<int64_t>(c + h * g.RT + rt) * g.slot_rows;
+      simt_rows<D>(
+          sm, k_prefix + h * p.prefix_hstride, v_prefix + h * p.prefix_hstride, (x - begin) * kSKeys,
+          min(plen, (end - begin) * kSKeys), p.sl2,
+          [&](int r) -> const float * {
+            const int bt = (row0 + r) / g.G, gg = (row0 + r) % g.G;
+            return row0 + r < g.R ? q + (static_cast<int64_t>(bt) * g.Hq + h * g.G + gg) * D : nullptr;
+          },
+          [&](int) { return plen; }, min(kSRows, g.R - row0), part_o + slot * D, part_l + slot);
+      x = end;
+    }
     return;
   }
-  const PrefixLine w = prefix_line(g, plen, gridDim.x);
-  const int c = blockIdx.x;
-  if (c >= w.n) return;
-  const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
-  int x = prefix_cta_begin(w, c);
-  const int x1 = prefix_cta_begin(w, c + 1);
-  while (x < x1) {
-    const int h = x / w.head;
-    const int rt = min((x - h * w.head) / w.nt, g.RT - 1);
-    const int begin = prefix_pair_begin(w, h, rt);
-    const int end = min(x1, begin + prefix_pair_steps(g, w, rt));
-    const int row0 = rt * kSRows;
-    __syncthreads();
-    for (int i = threadIdx.x; i < kSRows * (D / 4); i += kSThreads) {
-      const int r = i / (D / 4), d = 4 * (i % (D / 4));
-      float4 val = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (row0 + r < g.R) {
-        const int bt = (row0 + r) / g.G, gg = (row0 + r) % g.G;
-        val = load4(q + (static_cast<int64_t>(bt) * g.Hq + h * g.G + gg) * D + d);
-      }
-      *reinterpret_cast<float4 *>(sq + r * Lay::kStride + d) = val;
-    }
-    float m[4], l[4], acc[4][4 * NC];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      m[i] = -INFINITY;
-      l[i] = 0.f;
-#pragma unroll
-      for (int e = 0; e < 4 * NC; ++e) acc[i][e] = 0.f;
-    }
-    for (; x < end; ++x) {
-      const int key0 = (x - begin) * kSKeys;
-      const int nk = min(kSKeys, plen - key0);
-      __syncthreads();  // the tile before has been read
-      for (int i = threadIdx.x; i < kSKeys * (D / 4); i += kSThreads) {
-        const int r = i / (D / 4), d = 4 * (i % (D / 4));
-        float4 kk = make_float4(0.f, 0.f, 0.f, 0.f), vv = kk;  // rows past the prefix hold anything
-        if (r < nk) {
-          const int64_t off = h * head_stride + static_cast<int64_t>(key0 + r) * D + d;
-          kk = load4(k + off);
-          vv = load4(v + off);
-        }
-        *reinterpret_cast<float4 *>(sk + r * Lay::kStride + d) = kk;
-        *reinterpret_cast<float4 *>(sv + r * Lay::kStride + d) = vv;
-      }
-      __syncthreads();
-      float s[4][4] = {};
-      for (int d = 0; d < D; d += 4) {
-        float4 a[4], b[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) a[i] = *reinterpret_cast<const float4 *>(sq + (4 * ty + i) * Lay::kStride + d);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) b[j] = *reinterpret_cast<const float4 *>(sk + (tx + 16 * j) * Lay::kStride + d);
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            s[i][j] = fmaf(a[i].x, b[j].x, s[i][j]);
-            s[i][j] = fmaf(a[i].y, b[j].y, s[i][j]);
-            s[i][j] = fmaf(a[i].z, b[j].z, s[i][j]);
-            s[i][j] = fmaf(a[i].w, b[j].w, s[i][j]);
-          }
-      }
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        float mx = -INFINITY;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          s[i][j] = (tx + 16 * j < nk) ? s[i][j] * sl2 : -INFINITY;
-          mx = fmaxf(mx, s[i][j]);
-        }
-        mx = fmaxf(m[i], warp_max_xor(mx, 1, 8));
-        const float mu = (mx == -INFINITY) ? 0.f : mx;
-        const float alpha = exp2f(m[i] - mu);
-        float sum = 0.f;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float e = exp2f(s[i][j] - mu);
-          sum += e;
-          sp[(4 * ty + i) * Lay::kPStride + tx + 16 * j] = e;
-        }
-        l[i] = l[i] * alpha + warp_sum_xor(sum, 1, 8);
-        m[i] = mx;
-#pragma unroll
-        for (int e = 0; e < 4 * NC; ++e) acc[i][e] *= alpha;
-      }
-      __syncwarp();  // a row's 64 probabilities come from the 16 threads of its own half-warp
-      for (int j = 0; j < kSKeys; j += 4) {
-        float4 pr[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) pr[i] = *reinterpret_cast<const float4 *>(sp + (4 * ty + i) * Lay::kPStride + j);
-#pragma unroll
-        for (int jj = 0; jj < 4; ++jj)
-#pragma unroll
-          for (int cc = 0; cc < NC; ++cc) {
-            const float4 vv = *reinterpret_cast<const float4 *>(sv + (j + jj) * Lay::kStride + 64 * cc + 4 * tx);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const float pe = jj == 0 ? pr[i].x : jj == 1 ? pr[i].y : jj == 2 ? pr[i].z : pr[i].w;
-              acc[i][4 * cc] = fmaf(pe, vv.x, acc[i][4 * cc]);
-              acc[i][4 * cc + 1] = fmaf(pe, vv.y, acc[i][4 * cc + 1]);
-              acc[i][4 * cc + 2] = fmaf(pe, vv.z, acc[i][4 * cc + 2]);
-              acc[i][4 * cc + 3] = fmaf(pe, vv.w, acc[i][4 * cc + 3]);
-            }
-          }
-      }
-      __syncwarp();
-    }
-    const int64_t slot = c + h * g.RT + rt;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int r = 4 * ty + i;
-      if (row0 + r >= g.R) continue;
-      const float inv = l[i] > 0.f ? 1.f / l[i] : 0.f;
-#pragma unroll
-      for (int cc = 0; cc < NC; ++cc)
-        *reinterpret_cast<float4 *>(part_o + (slot * g.slot_rows + r) * D + 64 * cc + 4 * tx) =
-            make_float4(acc[i][4 * cc] * inv, acc[i][4 * cc + 1] * inv, acc[i][4 * cc + 2] * inv,
-                        acc[i][4 * cc + 3] * inv);
-      if (tx == 0) part_l[slot * g.slot_rows + r] = l[i] > 0.f ? (m[i] + log2f(l[i])) * kLn2 : -INFINITY;
-    }
-  }
+  const int unit = blockIdx.x - p.n_prefix, chunk = unit % own.count, pair = unit / own.count;
+  const int rt = pair % own.row_tiles, bh = pair / own.row_tiles;
+  const int h = bh % g.Hkv, b = bh / g.Hkv;
+  const int L = kv_len[b], key0 = chunk * own.keys, rows = g.T * g.G, row0 = rt * kSRows;
+  if (L < g.T || L > own.cap || key0 >= L) return;
+  const int64_t slot = static_cast<int64_t>(unit) * own.slot_rows, at = b * p.own_bstride + h * p.own_hstride;
+  simt_rows<D>(
+      sm, k_own + at, v_own + at, key0, min(L, key0 + own.keys), p.sl2,
+      [&](int r) -> const float * {
+        const int t = (row0 + r) / g.G, gg = (row0 + r) % g.G;
+        return row0 + r < rows ? q + ((static_cast<int64_t>(b) * g.T + t) * g.Hq + h * g.G + gg) * D : nullptr;
+      },
+      [&](int r) { return L - g.T + (row0 + r) / g.G + 1; }, min(kSRows, rows - row0), own_o + slot * D, own_l + slot);
 }
 
 // ---------------------------------------------------------------- merge
@@ -187,8 +229,8 @@ template <int D>
 __global__ void __launch_bounds__(kMergeThreads)
     prefix_merge_kernel(const float *__restrict__ own_o, const float *__restrict__ own_l,
                         const float *__restrict__ part_o, const float *__restrict__ part_l,
-                        const int32_t *__restrict__ prefix_len, PrefixGeom g, int grid, float *__restrict__ out_f32,
-                        __nv_bfloat16 *__restrict__ out_bf16, float *__restrict__ lse_out) {
+                        const int32_t *__restrict__ prefix_len, const int32_t *__restrict__ kv_len, PrefixGeom g,
+                        int grid, OwnChunks own, float *__restrict__ out_f32, __nv_bfloat16 *__restrict__ out_bf16, float *__restrict__ lse_out) {
   pdl_launch_dependents();
   pdl_wait();
   constexpr int kLanes = D / 4;
@@ -196,12 +238,37 @@ __global__ void __launch_bounds__(kMergeThreads)
   const int64_t row = static_cast<int64_t>(blockIdx.x) * (kMergeThreads / kLanes) + threadIdx.x / kLanes;  // (b, t, hq)
   if (row >= static_cast<int64_t>(g.B) * g.T * g.Hq) return;
   const int plen = prefix_len[0];
-  float m = own_l[row], sum = 1.f;
-  float4 o = *reinterpret_cast<const float4 *>(own_o + row * D + d);
+  const int hq = static_cast<int>(row % g.Hq), bt = static_cast<int>(row / g.Hq);
+  const int h = hq / g.G, gg = hq - h * g.G;
+  float m = -INFINITY, sum = 1.f;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  // one more partial result
+  auto add = [&](float l, const float4 &x) {
+    const float mn = fmaxf(m, l);
+    if (mn == -INFINITY) return;  // no finite score so far
+    const float a = expf(m - mn), b = expf(l - mn);
+    sum = sum * a + b;
+    o.x = o.x * a + x.x * b;
+    o.y = o.y * a + x.y * b;
+    o.z = o.z * a + x.z * b;
+    o.w = o.w * a + x.w * b;
+    m = mn;
+  };
+  if (own.count == 0) {  // one own result a row, in the rows' order
+    m = own_l[row];
+    o = *reinterpret_cast<const float4 *>(own_o + row * D + d);
+  } else {
+    const int b = bt / g.T, r = (bt - b * g.T) * g.G + gg;
+    const int n = min(own.count, (kv_len[b] + own.keys - 1) / own.keys);
+    const int64_t at = (static_cast<int64_t>(b * g.Hkv + h) * own.row_tiles + r / kSRows) * own.count * own.slot_rows + r % kSRows;
+    m = own_l[at];
+    o = *reinterpret_cast<const float4 *>(own_o + at * D + d);
+    for (int c = 1; c < n; ++c)
+      add(own_l[at + c * own.slot_rows], *reinterpret_cast<const float4 *>(own_o + (at + c * own.slot_rows) * D + d));
+  }
   if (plen < 0 || plen > g.prefix_cap) return;  // flagged by the prefix kernel
   if (plen > 0) {
-    const int hq = static_cast<int>(row % g.Hq), bt = static_cast<int>(row / g.Hq);
-    const int h = hq / g.G, r = bt * g.G + hq % g.G;
+    const int r = bt * g.G + gg;
     const int rt = r / g.tile_rows, lr = r % g.tile_rows;
     const PrefixLine w = prefix_line(g, plen, grid);
     const int begin = prefix_pair_begin(w, h, rt);
@@ -217,17 +284,8 @@ __global__ void __launch_bounds__(kMergeThreads)
         x[i] = __ldcg(reinterpret_cast<const float4 *>(part_o + at * D + d));
       }
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float mn = fmaxf(m, l[i]);
-        if (c + i > c1 || mn == -INFINITY) continue;  // past the last, or no finite score so far
-        const float a = expf(m - mn), b = expf(l[i] - mn);
-        sum = sum * a + b;
-        o.x = o.x * a + x[i].x * b;
-        o.y = o.y * a + x[i].y * b;
-        o.z = o.z * a + x[i].z * b;
-        o.w = o.w * a + x[i].w * b;
-        m = mn;
-      }
+      for (int i = 0; i < 4; ++i)
+        if (c + i <= c1) add(l[i], x[i]);
     }
   }
   const float inv = 1.f / sum;
@@ -243,25 +301,34 @@ __global__ void __launch_bounds__(kMergeThreads)
 }
 
 template <int D>
-cudaError_t simt_one(const PrefixPlan &p, const PrefixArgs &a) {
-  auto kern = prefix_simt_kernel<D>;
+cudaError_t simt_one(const PrefixPlan &p, const PrefixArgs &a, const AttnArgs &o) {
   constexpr int smem = SimtLayout<D>::bytes;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  cudaError_t e = want_shared_memory<prefix_simt_kernel<D>>(smem);
   if (e != cudaSuccess) return e;
+  SimtParams sp;
+  sp.g = p.g;
+  sp.own = p.chunks;
+  sp.n_prefix = p.grid;
+  sp.sl2 = a.sm_scale * kLog2e;
+  sp.prefix_hstride = a.head_stride;
+  sp.own_bstride = o.kv_batch_stride;
+  sp.own_hstride = o.kv_head_stride;
   unsigned char *ws = static_cast<unsigned char *>(a.ws);
-  return launch_pdl(kern, dim3(p.grid), dim3(kSThreads), smem, a.stream, static_cast<const float *>(a.q),
-                    static_cast<const float *>(a.k), static_cast<const float *>(a.v), a.prefix_len, a.head_stride,
-                    a.sm_scale * kLog2e, p.g, reinterpret_cast<float *>(ws + p.off_part_o),
-                    reinterpret_cast<float *>(ws + p.off_part_l), static_cast<WsHeader *>(a.ws));
+  return launch_pdl(prefix_simt_kernel<D>, dim3(p.grid + p.g.B * p.g.Hkv * p.chunks.row_tiles * p.chunks.count),
+                    dim3(kSThreads), smem, a.stream, static_cast<const float *>(a.q), static_cast<const float *>(a.k),
+                    static_cast<const float *>(a.v), a.prefix_len, static_cast<const float *>(o.k),
+                    static_cast<const float *>(o.v), o.kv_len, reinterpret_cast<float *>(ws + p.off_part_o),
+                    reinterpret_cast<float *>(ws + p.off_part_l), reinterpret_cast<float *>(ws + p.off_own_o),
+                    reinterpret_cast<float *>(ws + p.off_own_l), static_cast<WsHeader *>(a.ws), sp);
 }
 
 }  // namespace
 
-cudaError_t launch_prefix_simt(const PrefixPlan &p, const PrefixArgs &a) {
-  return p.g.D == 128 ? simt_one<128>(p, a) : simt_one<64>(p, a);
+cudaError_t launch_prefix_simt(const PrefixPlan &p, const PrefixArgs &a, const AttnArgs &own) {
+  return p.g.D == 128 ? simt_one<128>(p, a, own) : simt_one<64>(p, a, own);
 }
 
-cudaError_t launch_prefix_merge(const PrefixPlan &p, const PrefixArgs &a) {
+cudaError_t launch_prefix_merge(const PrefixPlan &p, const PrefixArgs &a, const int32_t *kv_len) {
   const unsigned char *ws = static_cast<const unsigned char *>(a.ws);
   const int64_t rows = static_cast<int64_t>(p.g.B) * p.g.T * p.g.Hq;
   const int per = kMergeThreads / (p.g.D / 4);
@@ -270,7 +337,7 @@ cudaError_t launch_prefix_merge(const PrefixPlan &p, const PrefixArgs &a) {
                     a.stream, reinterpret_cast<const float *>(ws + p.off_own_o),
                     reinterpret_cast<const float *>(ws + p.off_own_l),
                     reinterpret_cast<const float *>(ws + p.off_part_o),
-                    reinterpret_cast<const float *>(ws + p.off_part_l), a.prefix_len, p.g, p.grid,
+                    reinterpret_cast<const float *>(ws + p.off_part_l), a.prefix_len, kv_len, p.g, p.grid, p.chunks,
                     a.out_bf16 ? nullptr : static_cast<float *>(a.out),
                     a.out_bf16 ? static_cast<__nv_bfloat16 *>(a.out) : nullptr, a.lse);
 }
@@ -313,17 +380,26 @@ PrefixPlan plan_prefix(int B, int T, int Hq, int Hkv, int D, int prefix_cap, int
   g.RT = (g.R + g.tile_rows - 1) / g.tile_rows;
   g.last_half = !in_f32 && g.R - (g.RT - 1) * g.tile_rows <= 256;
   g.slot_rows = std::min(g.tile_rows, g.R);
-  p.own = plan_attention(B, T, Hq, Hkv, D, kv_cap, sm_count, !in_f32);
+  p.own = plan_attention(B, T, Hq, Hkv, D, kv_cap, sm_count, true);  // bf16
   p.own_cap = kv_cap;
   // what fits at once: two CTAs of 116 KB shared memory an SM; clusters of two CTAs of 226 KB
   p.grid = in_f32 ? 2 * sm_count : std::max(1, sm_count / 2);
-  const size_t rows = static_cast<size_t>(B) * T * Hq;
+  size_t own_rows = static_cast<size_t>(B) * T * Hq;
+  if (in_f32) {  // at most eight chunks of keys a sequence
+    OwnChunks &c = p.chunks;
+    c.cap = kv_cap;
+    c.keys = ((kv_cap + 7) / 8 + kSKeys - 1) / kSKeys * kSKeys;
+    c.count = (kv_cap + c.keys - 1) / c.keys;
+    c.row_tiles = (T * g.G + kSRows - 1) / kSRows;
+    c.slot_rows = std::min(kSRows, T * g.G);
+    own_rows = static_cast<size_t>(B) * Hkv * c.row_tiles * c.count * c.slot_rows;
+  }
   const size_t slots = static_cast<size_t>(p.grid) + static_cast<size_t>(Hkv) * g.RT;
   size_t off = align_up(p.own.ws_bytes);  // the own attention's scratch (and the header) comes first
   p.off_own_o = off;
-  off = align_up(off + rows * D * sizeof(float));
+  off = align_up(off + own_rows * D * sizeof(float));
   p.off_own_l = off;
-  off = align_up(off + rows * sizeof(float));
+  off = align_up(off + own_rows * sizeof(float));
   p.off_part_o = off;
   off = align_up(off + slots * g.slot_rows * D * sizeof(float));
   p.off_part_l = off;

@@ -710,14 +710,6 @@ __global__ void __launch_bounds__(kPThreads, 1)
   }
 }
 
-template <int D>
-cudaError_t prepare_kernel() {
-  auto kern = prefix_tc05_kernel<D>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, PLayout<D>::alloc);
-  if (e != cudaSuccess) return e;
-  return cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
-}
-
 // Clusters that fit the GPU at once (an SM without a partner holds none), at most `most`.
 template <int D>
 int clusters(int most) {
@@ -734,7 +726,7 @@ int clusters(int most) {
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     int n = 0;
-    if (prepare_kernel<D>() != cudaSuccess || cudaOccupancyMaxActiveClusters(&n, prefix_tc05_kernel<D>, &cfg) != cudaSuccess ||
+    if (want_shared_memory<prefix_tc05_kernel<D>>(PLayout<D>::alloc) != cudaSuccess || cudaOccupancyMaxActiveClusters(&n, prefix_tc05_kernel<D>, &cfg) != cudaSuccess ||
         n < 1) {
       cudaGetLastError();
       return 1 << 30;
@@ -747,7 +739,7 @@ int clusters(int most) {
 template <int D>
 cudaError_t launch_one(const PrefixPlan &pl, const PrefixArgs &a, const CUtensorMap &kmap, const CUtensorMap &vmap,
                        const CUtensorMap *qmap) {
-  cudaError_t e = prepare_kernel<D>();
+  cudaError_t e = want_shared_memory<prefix_tc05_kernel<D>>(PLayout<D>::alloc);
   if (e != cudaSuccess) return e;
   PParams kp;
   kp.g = pl.g;

@@ -102,9 +102,7 @@ def status_name(s):
 
 
 def _ptr(x):
-    if x is None:
-        return None
-    if isinstance(x, int):
+    if x is None or type(x) is int:
         return x
     return x.data_ptr()
 
@@ -112,7 +110,8 @@ def _ptr(x):
 def _stream(s):
     if s is None:
         import torch
-        return torch.cuda.current_stream().cuda_stream
+        # the raw handle of torch.cuda.current_stream(), without the object around it (5 us a call)
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if isinstance(s, int):
         return s
     return s.cuda_stream
@@ -266,10 +265,12 @@ def mgd_prefix_workspace_size(B, T, Hq, Hkv, D, prefix_cap, kv_cap):
 def mgd_prefix_attn(q, k_prefix, v_prefix, prefix_len, prefix_cap, prefix_head_stride, k, v, kv_len, B, T, Hq, Hkv, D,
                     kv_cap, kv_batch_stride, kv_head_stride, sm_scale, in_dtype, out, out_dtype, lse, ws, ws_bytes,
                     stream=None):
-    _check(load().mgd_prefix_attn(_ptr(q), _ptr(k_prefix), _ptr(v_prefix), _ptr(prefix_len), prefix_cap,
-                                  prefix_head_stride, _ptr(k), _ptr(v), _ptr(kv_len), B, T, Hq, Hkv, D, kv_cap,
-                                  kv_batch_stride, kv_head_stride, sm_scale, in_dtype, _ptr(out), out_dtype, _ptr(lse),
-                                  _ptr(ws), ws_bytes, _stream(stream)))
+    status = (_lib or load()).mgd_prefix_attn(
+        _ptr(q), _ptr(k_prefix), _ptr(v_prefix), _ptr(prefix_len), prefix_cap, prefix_head_stride, _ptr(k), _ptr(v),
+        _ptr(kv_len), B, T, Hq, Hkv, D, kv_cap, kv_batch_stride, kv_head_stride, sm_scale, in_dtype, _ptr(out), out_dtype,
+        _ptr(lse), _ptr(ws), ws_bytes, _stream(stream))
+    if status:
+        _check(status)
 
 
 def mgd_rope_frequencies(rotary_dim, base, scaling, params=None):
@@ -288,11 +289,12 @@ def mgd_rope_workspace_size(B):
 def mgd_rope_append(q, q_token_stride, k_new, k_token_stride, v_new, v_token_stride, turns, magnitude, rotary_dim,
                     interleaved, B, T, Hq, Hkv, D, dtype, kv_len, new_len, pos_offset, pos_offset_stride, q_out, k, v,
                     kv_cap, kv_batch_stride, kv_head_stride, ws, ws_bytes, stream=None):
-    _check(load().mgd_rope_append(_ptr(q), q_token_stride, _ptr(k_new), k_token_stride, _ptr(v_new), v_token_stride,
-                                  _ptr(turns), magnitude, rotary_dim, interleaved, B, T, Hq, Hkv, D, dtype,
-                                  _ptr(kv_len), _ptr(new_len), _ptr(pos_offset), pos_offset_stride, _ptr(q_out),
-                                  _ptr(k), _ptr(v), kv_cap, kv_batch_stride, kv_head_stride, _ptr(ws), ws_bytes,
-                                  _stream(stream)))
+    status = (_lib or load()).mgd_rope_append(
+        _ptr(q), q_token_stride, _ptr(k_new), k_token_stride, _ptr(v_new), v_token_stride, _ptr(turns), magnitude,
+        rotary_dim, interleaved, B, T, Hq, Hkv, D, dtype, _ptr(kv_len), _ptr(new_len), _ptr(pos_offset), pos_offset_stride,
+        _ptr(q_out), _ptr(k), _ptr(v), kv_cap, kv_batch_stride, kv_head_stride, _ptr(ws), ws_bytes, _stream(stream))
+    if status:
+        _check(status)
 
 
 def mgd_logprobs_workspace_size(R, V, K):
@@ -301,6 +303,8 @@ def mgd_logprobs_workspace_size(R, V, K):
 
 def mgd_token_logprobs(logits, row_stride, dtype, tokens, R, V, K, logprob, entropy, rank, top_ids, top_logprobs, ws,
                        ws_bytes, stream=None):
-    _check(load().mgd_token_logprobs(_ptr(logits), row_stride, dtype, _ptr(tokens), R, V, K, _ptr(logprob),
-                                     _ptr(entropy), _ptr(rank), _ptr(top_ids), _ptr(top_logprobs), _ptr(ws), ws_bytes,
-                                     _stream(stream)))
+    status = (_lib or load()).mgd_token_logprobs(
+        _ptr(logits), row_stride, dtype, _ptr(tokens), R, V, K, _ptr(logprob), _ptr(entropy), _ptr(rank), _ptr(top_ids),
+        _ptr(top_logprobs), _ptr(ws), ws_bytes, _stream(stream))
+    if status:
+        _check(status)

@@ -43,9 +43,10 @@ def _check(device, dense=(), int32=(), f32=(), same=()):
 
 
 def _kv_strides(k, v, D):
-    if k.stride(3) != 1 or k.stride(2) != D or k.stride() != v.stride():
+    s = k.stride()
+    if s[3] != 1 or s[2] != D or s != v.stride():
         raise ValueError("K and V must share strides with contiguous rows of D elements")
-    return k.stride(0), k.stride(1)
+    return s[0], s[1]
 
 
 def workspace(nbytes, device):
@@ -250,40 +251,61 @@ def streaming_select(k, v, kv_len, sink, K, draft_cap=None, out=None, stream=Non
     return out
 
 
+def _as_wanted(device, dense, int32, f32, same):
+    """Whether _check() would pass, without its lists of names (it is called to say what is wrong)."""
+    where, d0 = device.index, same[0].dtype if same else None
+    for t in dense:
+        if t is not None and not (t.is_contiguous() and t.get_device() == where):
+            return False
+    for t in int32:
+        if t is not None and t.dtype is not torch.int32:
+            return False
+    for t in f32:
+        if t is not None and t.dtype is not torch.float32:
+            return False
+    for t in same:
+        if t.dtype is not d0 or t.get_device() != where:
+            return False
+    return True
+
+
 def prefix_attn(q, k_prefix, v_prefix, prefix_len, k, v, kv_len, sm_scale=None, out_dtype=torch.float32, ws=None,
                 out=None, lse=None, stream=None):
     """Verify (T = 1: draft) attention of a batch over a prefix that all its sequences share and each
     sequence's own rows behind it: q [B,T,Hq,D] (or [B,Hq,D]), k/v_prefix [Hkv,prefix_cap,D], prefix_len [1]
     int32, own k/v [B,Hkv,kv_cap,D], kv_len [B] int32 -> (out [B,T,Hq,D], lse [B,T,Hq]) (without T for a 3-d q).
     The prefix is read once for the whole batch."""
-    if q.dim() == 3:
-        shape, q = q.shape, q[:, None]
+    shape, dev = q.shape, q.device
+    if len(shape) == 3:
+        B, Hq, D = shape
+        T = 1
     else:
-        shape = q.shape
-    B, T, Hq, D = q.shape
-    Hkv, cap = k.shape[1], k.shape[2]
-    if k_prefix.dim() != 3 or k_prefix.shape[0] != Hkv or k_prefix.shape[2] != D or v_prefix.shape != k_prefix.shape:
+        B, T, Hq, D = shape
+    kshape, pshape = k.shape, k_prefix.shape
+    Hkv, cap = kshape[1], kshape[2]
+    if len(pshape) != 3 or pshape[0] != Hkv or pshape[2] != D or v_prefix.shape != pshape:
         raise ValueError("k_prefix and v_prefix must be [Hkv, prefix_cap, D] = [%d, *, %d]" % (Hkv, D))
-    if k_prefix.stride(2) != 1 or k_prefix.stride(1) != D or k_prefix.stride() != v_prefix.stride():
+    ps = k_prefix.stride()
+    if ps[2] != 1 or ps[1] != D or ps != v_prefix.stride():
         raise ValueError("prefix K and V must share strides with contiguous rows of D elements")
-    if k.shape[0] != B or k.shape[3] != D or v.shape != k.shape or kv_len.numel() != B or prefix_len.numel() != 1:
+    if kshape[0] != B or kshape[3] != D or v.shape != kshape or kv_len.numel() != B or prefix_len.numel() != 1:
         raise ValueError("k, v must be [B, Hkv, kv_cap, D], kv_len [B] and prefix_len [1]")
     sb, sh = _kv_strides(k, v, D)
     scale = 1.0 / math.sqrt(D) if sm_scale is None else sm_scale
     if out is None:
-        out = torch.empty(shape, dtype=out_dtype, device=q.device)
+        out = torch.empty(shape, dtype=out_dtype, device=dev)
     if lse is None:
-        lse = torch.empty(shape[:-1], dtype=torch.float32, device=q.device)
+        lse = torch.empty(shape[:-1], dtype=torch.float32, device=dev)
     if out.shape != shape or lse.shape != shape[:-1]:
         raise ValueError("out must have q's shape and lse the same without D")
-    _check(q.device, dense=[("q", q), ("kv_len", kv_len), ("prefix_len", prefix_len), ("out", out), ("lse", lse)],
-           int32=[("kv_len", kv_len), ("prefix_len", prefix_len)], f32=[("lse", lse)],
-           same=[("q", q), ("k_prefix", k_prefix), ("v_prefix", v_prefix), ("k", k), ("v", v)])
-    pcap = k_prefix.shape[1]
+    if not _as_wanted(dev, (q, kv_len, prefix_len, out, lse), (kv_len, prefix_len), (lse,), (q, k_prefix, v_prefix, k, v)):
+        _check(dev, dense=[("q", q), ("kv_len", kv_len), ("prefix_len", prefix_len), ("out", out), ("lse", lse)],
+               int32=[("kv_len", kv_len), ("prefix_len", prefix_len)], f32=[("lse", lse)],
+               same=[("q", q), ("k_prefix", k_prefix), ("v_prefix", v_prefix), ("k", k), ("v", v)])
     if ws is None:
-        ws = workspace(mgd.mgd_prefix_workspace_size(B, T, Hq, Hkv, D, pcap, cap), q.device)
-    mgd.mgd_prefix_attn(q, k_prefix, v_prefix, prefix_len, pcap, k_prefix.stride(0), k, v, kv_len, B, T, Hq, Hkv, D,
-                        cap, sb, sh, scale, _dtype_code(q), out, _dtype_code(out), lse, ws, ws.numel(), stream)
+        ws = workspace(mgd.mgd_prefix_workspace_size(B, T, Hq, Hkv, D, pshape[1], cap), dev)
+    mgd.mgd_prefix_attn(q, k_prefix, v_prefix, prefix_len, pshape[1], ps[0], k, v, kv_len, B, T, Hq, Hkv, D, cap, sb, sh,
+                        scale, _dtype_code(q), out, _dtype_code(out), lse, ws, ws.numel(), stream)
     return out, lse
 
 
@@ -318,12 +340,13 @@ def rope_table(rotary_dim, base=10000.0, scaling=None, device="cuda"):
 
 def _token_stride(name, x, B, T, H, D):
     """Elements between two tokens' heads of a [B, T, H, D] tensor that may be a view of a fused projection."""
-    if x.dim() != 4 or tuple(x.shape) != (B, T, H, D):
+    if x.shape != (B, T, H, D):
         raise ValueError("%s must be [%d, %d, %d, %d], got %s" % (name, B, T, H, D, tuple(x.shape)))
-    if x.stride(3) != 1 or (H > 1 and x.stride(2) != D):
+    s = x.stride()
+    if s[3] != 1 or (H > 1 and s[2] != D):
         raise ValueError("%s must hold a token's heads packed" % name)
-    step = x.stride(1) if T > 1 else x.stride(0) if B > 1 else H * D
-    if B > 1 and T > 1 and x.stride(0) != T * step:
+    step = s[1] if T > 1 else s[0] if B > 1 else H * D
+    if B > 1 and T > 1 and s[0] != T * step:
         raise ValueError("%s must hold its tokens at one stride" % name)
     return step
 
@@ -335,31 +358,35 @@ def rope_append(q, k_new, v_new, table, k, v, kv_len, new_len=None, pos_offset=N
     the turned q (q_out; contiguous).  kv_len [B] int32 counts the new rows; new_len [B] int32 (default T each);
     pos_offset [1] or [B] int32 is added to the row index to give the position."""
     B, T, Hq, D = q.shape
-    Hkv, cap = k.shape[1], k.shape[2]
-    if k.shape[0] != B or k.shape[3] != D or v.shape != k.shape or kv_len.numel() != B:
+    kshape, dev, turns = k.shape, q.device, table.turns
+    Hkv, cap = kshape[1], kshape[2]
+    if kshape[0] != B or kshape[3] != D or v.shape != kshape or kv_len.numel() != B:
         raise ValueError("k, v must be [B, Hkv, kv_cap, D] and kv_len [B]")
-    sq, sk, sv = (_token_stride(n, x, B, T, h, D) for n, x, h in
-                  (("q", q, Hq), ("k_new", k_new, Hkv), ("v_new", v_new, Hkv)))
+    sq = _token_stride("q", q, B, T, Hq, D)
+    sk = _token_stride("k_new", k_new, B, T, Hkv, D)
+    sv = _token_stride("v_new", v_new, B, T, Hkv, D)
     sb, sh = _kv_strides(k, v, D)
     if new_len is not None and new_len.numel() != B:
         raise ValueError("new_len must be [B]")
-    if pos_offset is not None and pos_offset.numel() not in (1, B):
+    offsets = 0 if pos_offset is None else pos_offset.numel()
+    if pos_offset is not None and offsets not in (1, B):
         raise ValueError("pos_offset must be [1] or [B]")
     if q_out is None:
-        q_out = torch.zeros((B, T, Hq, D), dtype=q.dtype, device=q.device)
+        q_out = torch.zeros((B, T, Hq, D), dtype=q.dtype, device=dev)
     if q_out.shape != q.shape:
         raise ValueError("q_out must have q's shape")
-    if table.turns.dtype != torch.int64 or table.turns.numel() != table.rotary_dim // 2:
+    if turns.dtype is not torch.int64 or turns.numel() != table.rotary_dim // 2:
         raise TypeError("table must come from rope_table")
-    _check(q.device, dense=[("kv_len", kv_len), ("new_len", new_len), ("pos_offset", pos_offset), ("q_out", q_out),
-                            ("table", table.turns)],
-           int32=[("kv_len", kv_len), ("new_len", new_len), ("pos_offset", pos_offset)],
-           same=[("q", q), ("k_new", k_new), ("v_new", v_new), ("k", k), ("v", v), ("q_out", q_out)])
+    if not _as_wanted(dev, (kv_len, new_len, pos_offset, q_out, turns), (kv_len, new_len, pos_offset), (),
+                      (q, k_new, v_new, k, v, q_out)):
+        _check(dev, dense=[("kv_len", kv_len), ("new_len", new_len), ("pos_offset", pos_offset), ("q_out", q_out),
+                           ("table", turns)],
+               int32=[("kv_len", kv_len), ("new_len", new_len), ("pos_offset", pos_offset)],
+               same=[("q", q), ("k_new", k_new), ("v_new", v_new), ("k", k), ("v", v), ("q_out", q_out)])
     if ws is None:
-        ws = workspace(mgd.mgd_rope_workspace_size(B), q.device)
-    stride = 0 if pos_offset is None or pos_offset.numel() == 1 else 1
-    mgd.mgd_rope_append(q, sq, k_new, sk, v_new, sv, table.turns, table.magnitude, table.rotary_dim, int(interleaved),
-                        B, T, Hq, Hkv, D, _dtype_code(q), kv_len, new_len, pos_offset, stride, q_out, k, v, cap, sb,
+        ws = workspace(mgd.mgd_rope_workspace_size(B), dev)
+    mgd.mgd_rope_append(q, sq, k_new, sk, v_new, sv, turns, table.magnitude, table.rotary_dim, int(interleaved), B, T, Hq,
+                        Hkv, D, _dtype_code(q), kv_len, new_len, pos_offset, 1 if offsets > 1 else 0, q_out, k, v, cap, sb,
                         sh, ws, ws.numel(), stream)
     return q_out
 
@@ -368,34 +395,38 @@ def token_logprobs(logits, tokens, top=0, ws=None, out=None, stream=None):
     """Log probabilities of `tokens` [...] int32 (-1: no token) under softmax(logits [..., V], float32 or
     bfloat16; rows at one stride).  Returns dict(logprob [...], entropy [...] float32, rank [...] int32,
     top_ids [..., top] int32, top_logprobs [..., top] float32)."""
-    V = logits.shape[-1]
-    if tokens.shape != logits.shape[:-1]:
+    shape, strides = logits.shape, logits.stride()
+    V, lead = shape[-1], tokens.shape
+    if lead != shape[:-1]:
         raise ValueError("tokens must have the shape of logits without its last dimension")
-    R = tokens.numel()
-    if V > 1 and logits.stride(-1) != 1:
+    R, dev = tokens.numel(), logits.device
+    if V > 1 and strides[-1] != 1:
         raise ValueError("logits must hold a row's entries packed")
-    dims = [(n, s) for n, s in zip(logits.shape[:-1], logits.stride()[:-1]) if n > 1]
-    step = dims[-1][1] if dims else V
-    rows = 1
-    for n, s in reversed(dims):
-        if s != step * rows:
-            raise ValueError("logits must hold its rows at one stride")
-        rows *= n
-    dev, lead = logits.device, tuple(tokens.shape)
+    step, rows = 0, 1  # elements from one row to the next, and rows of the dimensions seen from behind
+    for n, s in zip(shape[-2::-1], strides[-2::-1]):
+        if n > 1:
+            step = step or s
+            if s != step * rows:
+                raise ValueError("logits must hold its rows at one stride")
+            rows *= n
     if out is None:
         out = dict(logprob=torch.empty(lead, dtype=torch.float32, device=dev),
                    entropy=torch.empty(lead, dtype=torch.float32, device=dev),
                    rank=torch.empty(lead, dtype=torch.int32, device=dev),
-                   top_ids=torch.empty(lead + (top,), dtype=torch.int32, device=dev),
-                   top_logprobs=torch.empty(lead + (top,), dtype=torch.float32, device=dev))
-    for name in ("logprob", "entropy", "rank", "top_ids", "top_logprobs"):
-        if tuple(out[name].shape) != (lead + (top,) if name.startswith("top") else lead):
+                   top_ids=torch.empty((*lead, top), dtype=torch.int32, device=dev),
+                   top_logprobs=torch.empty((*lead, top), dtype=torch.float32, device=dev))
+    logprob, entropy, rank, ids, lps = (out["logprob"], out["entropy"], out["rank"], out["top_ids"], out["top_logprobs"])
+    tops = (*lead, top)
+    for name, want in (("logprob", lead), ("entropy", lead), ("rank", lead), ("top_ids", tops), ("top_logprobs", tops)):
+        if out[name].shape != want:
             raise ValueError("out[%r] has the wrong shape" % name)
-    ints = [("tokens", tokens), ("rank", out["rank"]), ("top_ids", out["top_ids"])]
-    floats = [(n, out[n]) for n in ("logprob", "entropy", "top_logprobs")]
-    _check(dev, dense=ints + floats, int32=ints, f32=floats)
+    if not _as_wanted(dev, (tokens, logprob, entropy, rank, ids, lps), (tokens, rank, ids), (logprob, entropy, lps),
+                      (logits,)):
+        ints = [("tokens", tokens), ("rank", rank), ("top_ids", ids)]
+        floats = [("logprob", logprob), ("entropy", entropy), ("top_logprobs", lps)]
+        _check(dev, dense=ints + floats, int32=ints, f32=floats)
     if ws is None:
         ws = workspace(mgd.mgd_logprobs_workspace_size(R, V, top), dev)
-    mgd.mgd_token_logprobs(logits, step, _dtype_code(logits), tokens, R, V, top, out["logprob"], out["entropy"],
-                           out["rank"], out["top_ids"], out["top_logprobs"], ws, ws.numel(), stream)
+    mgd.mgd_token_logprobs(logits, step or V, _dtype_code(logits), tokens, R, V, top, logprob, entropy, rank, ids, lps, ws,
+                           ws.numel(), stream)
     return out

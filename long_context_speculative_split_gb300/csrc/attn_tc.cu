@@ -95,7 +95,7 @@ __global__ void __launch_bounds__(kThreads, MINB)
                    const __nv_bfloat16 *__restrict__ q, const int32_t *__restrict__ kv_len,
                    float *__restrict__ out_f32, __nv_bfloat16 *__restrict__ out_bf16, float *__restrict__ lse_out,
                    unsigned char *__restrict__ ws, KParams p) {
-  if constexpr (!kBeside) pdl_launch_dependents();
+  pdl_launch_dependents();
   using Lay = Layout<D, NT>;
   extern __shared__ unsigned char smem_raw[];
   unsigned char *smem = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -226,10 +226,7 @@ __global__ void __launch_bounds__(kThreads, MINB)
     // This CTA's claims are over: it checks in (its consumers need not: they claim nothing,
     // and their only error bits, timeouts, land in one of the two words either way).
     // From a ready header the counter hands out exactly the units past the first wave.
-    if constexpr (kBeside) {  // the next kernel waits for this one alone: it ends after the prefix kernel
-      pdl_wait();
-      pdl_launch_dependents();
-    }
+    if constexpr (kBeside) pdl_wait();  // the next kernel waits for this one alone: it ends after the prefix kernel
     call_check_in(hdr, gridDim.x, blockIdx.x, claims, p.total_units - firsts);
     return;
   }

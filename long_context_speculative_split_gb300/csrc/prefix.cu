@@ -164,8 +164,8 @@ __global__ void __launch_bounds__(kSThreads)
                        const float *__restrict__ k_own, const float *__restrict__ v_own,
                        const int32_t *__restrict__ kv_len, float *__restrict__ part_o, float *__restrict__ part_l,
                        float *__restrict__ own_o, float *__restrict__ own_l, WsHeader *hdr, SimtParams p) {
-  pdl_launch_dependents();
   pdl_wait();
+  pdl_launch_dependents();  // after the wait: the merge reads prefix_len before its own
   extern __shared__ float sm[];
   const PrefixGeom &g = p.g;
   const OwnChunks &own = p.own;
@@ -232,14 +232,29 @@ __global__ void __launch_bounds__(kMergeThreads)
                         const int32_t *__restrict__ prefix_len, const int32_t *__restrict__ kv_len, PrefixGeom g,
                         int grid, OwnChunks own, float *__restrict__ out_f32, __nv_bfloat16 *__restrict__ out_bf16, float *__restrict__ lse_out) {
   pdl_launch_dependents();
-  pdl_wait();
   constexpr int kLanes = D / 4;
   const int d = 4 * (threadIdx.x % kLanes);
   const int64_t row = static_cast<int64_t>(blockIdx.x) * (kMergeThreads / kLanes) + threadIdx.x / kLanes;  // (b, t, hq)
-  if (row >= static_cast<int64_t>(g.B) * g.T * g.Hq) return;
+  // The length and the places come before the wait: the kernels before this one let it start only after
+  // their own wait for whatever wrote the call's inputs.
   const int plen = prefix_len[0];
-  const int hq = static_cast<int>(row % g.Hq), bt = static_cast<int>(row / g.Hq);
+  const int bt = row >> 31 ? static_cast<int>(row / g.Hq) : static_cast<int>(row) / g.Hq;
+  const int hq = static_cast<int>(row - static_cast<int64_t>(bt) * g.Hq);
   const int h = hq / g.G, gg = hq - h * g.G;
+  const bool valid = plen >= 0 && plen <= g.prefix_cap;  // else: flagged by the prefix kernel
+  int c0 = 0, c1 = -1;
+  int64_t at0 = 0;
+  if (valid && plen > 0) {
+    const int r = bt * g.G + gg;
+    const int rt = r / g.tile_rows, lr = r % g.tile_rows;
+    const PrefixLine w = prefix_line(g, plen, grid);
+    const int begin = prefix_pair_begin(w, h, rt);
+    c0 = prefix_cta_of(w, begin);
+    c1 = prefix_cta_of(w, begin + prefix_pair_steps(g, w, rt) - 1);
+    at0 = static_cast<int64_t>(h * g.RT + rt) * g.slot_rows + lr;
+  }
+  pdl_wait();
+  if (!valid || row >= static_cast<int64_t>(g.B) * g.T * g.Hq) return;
   float m = -INFINITY, sum = 1.f;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
   // one more partial result
@@ -255,8 +270,8 @@ __global__ void __launch_bounds__(kMergeThreads)
     m = mn;
   };
   if (own.count == 0) {  // one own result a row, in the rows' order
-    m = own_l[row];
-    o = *reinterpret_cast<const float4 *>(own_o + row * D + d);
+    m = __ldcg(own_l + row);
+    o = __ldcg(reinterpret_cast<const float4 *>(own_o + row * D + d));
   } else {
     const int b = bt / g.T, r = (bt - b * g.T) * g.G + gg;
     const int n = min(own.count, (kv_len[b] + own.keys - 1) / own.keys);
@@ -266,27 +281,19 @@ __global__ void __launch_bounds__(kMergeThreads)
     for (int c = 1; c < n; ++c)
       add(own_l[at + c * own.slot_rows], *reinterpret_cast<const float4 *>(own_o + (at + c * own.slot_rows) * D + d));
   }
-  if (plen < 0 || plen > g.prefix_cap) return;  // flagged by the prefix kernel
-  if (plen > 0) {
-    const int r = bt * g.G + gg;
-    const int rt = r / g.tile_rows, lr = r % g.tile_rows;
-    const PrefixLine w = prefix_line(g, plen, grid);
-    const int begin = prefix_pair_begin(w, h, rt);
-    const int c0 = prefix_cta_of(w, begin), c1 = prefix_cta_of(w, begin + prefix_pair_steps(g, w, rt) - 1);
-    const int64_t at0 = static_cast<int64_t>(h * g.RT + rt) * g.slot_rows + lr;
-    for (int c = c0; c <= c1; c += 4) {  // four partial results on their way at once
-      float l[4];
-      float4 x[4];
+  for (int c = c0; c <= c1; c += 4) {  // four partial results on their way at once
+    float l[4];
+    float4 x[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int64_t at = at0 + static_cast<int64_t>(min(c + i, c1)) * g.slot_rows;
+    for (int i = 0; i < 4; ++i)
+      if (c + i <= c1) {
+        const int64_t at = at0 + static_cast<int64_t>(c + i) * g.slot_rows;
         l[i] = __ldcg(part_l + at);
         x[i] = __ldcg(reinterpret_cast<const float4 *>(part_o + at * D + d));
       }
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (c + i <= c1) add(l[i], x[i]);
-    }
+    for (int i = 0; i < 4; ++i)
+      if (c + i <= c1) add(l[i], x[i]);
   }
   const float inv = 1.f / sum;
   o.x *= inv;
@@ -343,19 +350,24 @@ cudaError_t launch_prefix_merge(const PrefixPlan &p, const PrefixArgs &a, const 
 }
 
 // The prefix kernel is bound by its tensor cores and their latency, the attention over the own caches by
-// HBM, so the prefix kernel takes only part of the SMs and the other one runs beside it.  Its clusters
-// out of `most`: the number that by these measured rates ends both first -- 1.7 us a step, 100 GB/s of
-// own cache an SM, 6600 GB/s in all -- with the capacities in place of the lengths, which only the device
-// knows.
+// its own SMs, so the prefix kernel takes only part of the SMs and the other one runs beside it.  Its
+// clusters out of `most`: the number that by these measured rates ends both first, with the capacities in
+// place of the lengths, which only the device knows.  Prefix: 6 us, 1.8 us a step and 2 us for every
+// further pair that a cluster has a part of (none where all parts end with a pair).  Own caches: from 6 us
+// on 55 GB/s an SM; what is left when the prefix kernel ends takes 8 us (a sequence) and 6.1 TB/s.
+// Measured against all pairs of SMs for the prefix kernel and the rest after it: 39.1 to 48.6 us for 128
+// new rows on 8192 shared keys with up to 512 own keys each, 326 to 333 us for 640 rows on 32768.
 int prefix_share(const PrefixPlan &p, int most, int sm_count) {
   const PrefixLine line = prefix_line(p.g, p.g.prefix_cap, most);
   const double own = 4.0 * p.g.B * p.g.Hkv * p.own_cap * p.g.D;  // bytes of K and V
   double best = 0.0;
   int share = most;
-  for (int n = most; n >= (most + 1) / 2; --n) {
-    const double prefix_us = 1.7 * ((line.total + n - 1) / n);
-    const double beside = 0.1e6 * (sm_count - 2 * n) * prefix_us;
-    const double us = prefix_us + (own > beside ? (own - beside) / 6.6e6 : 0.0);
+  for (int n = most; n >= (most + 2) / 3; --n) {
+    const int steps = (line.total + n - 1) / n;
+    const bool even = line.total % n == 0 && line.nt % steps == 0 && line.last % steps == 0;
+    const double prefix_us = 6.0 + 1.8 * steps + (even ? 0.0 : 2.0 * ((steps + line.nt - 1) / line.nt));
+    const double beside = 0.055e6 * (sm_count - 2 * n) * (prefix_us - 6.0);
+    const double us = prefix_us + (own > beside ? 8.0 + (own - beside) / 6.1e6 : 0.0);
     if (n == most || us < best) {
       best = us;
       share = n;

@@ -42,7 +42,8 @@ __host__ __device__ inline int prefix_cta_begin(const PrefixLine &w, int c) {
 }
 // The CTA whose part holds step x.
 __host__ __device__ inline int prefix_cta_of(const PrefixLine &w, int x) {
-  return static_cast<int>(((static_cast<int64_t>(x) + 1) * w.n - 1) / w.total);
+  const uint64_t a = (static_cast<uint64_t>(x) + 1) * w.n - 1;  // the quotient of 32-bit numbers is far cheaper
+  return static_cast<int>(a >> 32 ? a / w.total : static_cast<uint32_t>(a) / static_cast<uint32_t>(w.total));
 }
 __host__ __device__ inline int prefix_pair_begin(const PrefixLine &w, int h, int rt) { return h * w.head + rt * w.nt; }
 __host__ __device__ inline int prefix_pair_steps(const PrefixGeom &g, const PrefixLine &w, int rt) {

@@ -9,17 +9,21 @@
 // ascending unsigned number, then the complement of the index, so no two keys
 // are equal and ties need no rule of their own.
 //
-// Bound by HBM.  A cluster of up to 8 CTAs shares a row, and the clusters that fit the GPU
-// walk the rows that have a token.  Blocks of 32 KB come by bulk copies into two stages of
-// shared memory, one on its way while one is worked on, across rows as well.  Each thread
-// takes 128 bytes of a block, folds them into its own running sums (relative to its
-// own maximum), counts those before the token, and puts aside
-// those that can be alternatives: of the 64 groups of 4 threads, each with its largest
-// value, the K-th largest of these values bounds the K-th best entry from below, so a
-// handful more than K entries of the first block are put aside, and of later ones those
-// above that bound.  A list that has grown is put in order and cut to the best K, which
-// raises the bound.  (Where ties or sorted rows leave more than the list holds, the CTA
-// takes the maximum K times.)  The parts meet in the first CTA's shared memory.
+// Bound by HBM, and by the instructions of an entry close behind it.  A cluster of up to 8 CTAs
+// shares a row, and the clusters that fit the GPU walk the rows that have a token.  Blocks of 32 KB
+// come by bulk copies into two stages of shared memory, one on its way while one is worked on,
+// across rows as well.  Each thread takes 128 bytes of a block, folds them into its own running sums
+// (relative to its own maximum), counts those before the token and notes their largest.
+// The alternatives are chosen once in 8 blocks: of the 64 groups of 4 threads, each with its largest
+// value, the K-th largest of these values bounds the K-th best entry from below, so a handful more
+// than K of the threads' parts of blocks hold an entry at or above it.  Only those are looked at
+// again, and what they have above the bound is put in order.  (Where ties or sorted rows leave more
+// than the lists hold, the CTA takes the maximum K times.)  The parts meet in the first CTA's shared
+// memory.
+//
+// Measured at V = 128256: 2048 bfloat16 rows with 20 alternatives 132 us, 4.0 TB/s (choosing
+// in every block: 164 us; without the choice: about 120 us; two CTAs of 384 threads an SM: 154 us,
+// five of 128: 137 us); 384 float32 rows of 640 with 8 alternatives 42 us, 4.7 TB/s; 4 rows 10.6 us.
 #include <algorithm>
 
 #include "common.cuh"
@@ -33,10 +37,12 @@ constexpr int kLpLoads = 8;                       // 16-byte chunks of a thread 
 constexpr int kLpChunks = kLpThreads * kLpLoads;  // chunks of a block
 constexpr int kLpStages = 2;
 constexpr int kLpRows = 4;                        // rows listed ahead
+constexpr int kLpWalk = 8;                        // loads of 32 tokens at once in the search for a row
 constexpr int kLpStageBytes = kLpChunks * 16;
 constexpr int kLpGroups = 64;                     // groups of threads, the candidates for the bound
-constexpr int kLpList = 512;                      // entries put aside
-constexpr int kLpCut = 56;                        // a list longer than this is cut to the best K
+constexpr int kLpSpan = 8;                        // blocks between two choices of alternatives
+constexpr int kLpHits = 256;                      // threads' parts of blocks looked at again
+constexpr int kLpList = 256;                      // entries put aside; also the best of a cluster
 constexpr int kLpMaxK = 32;                       // kLpGroups bounds it
 constexpr int kLpMaxCluster = 8;
 constexpr float kLog2e = 1.4426950408889634f;
@@ -73,9 +79,12 @@ struct LpShared {
   RowPart part[kLpMaxCluster];
   RowPart warp[kLpThreads / 32];
   float group[kLpGroups];
+  __nv_bfloat16 top[kLpSpan][kLpThreads];  // the largest of a thread's entries in a block, or just above it
+  unsigned short hit[kLpHits];             // block of the span and thread
   float floor;     // no alternative is below this value
-  int count;
+  int hits, count;
   int64_t found[kLpRows];    // rows of this cluster that are to come
+  int token[kLpRows];        // their tokens
   uint64_t full[kLpStages];  // mbarriers: a block has landed
   int gave_up;
 };
@@ -119,15 +128,20 @@ struct Entries<float> {
     }
     return fmax3_nan(m[0], m[1], m[1]);
   }
-  // entries above a threshold, summed over the chunks of a block
-  using Count = int;
+  // entries above a threshold, summed over the chunks of a block: ones and sums as floats, two at a time
+  struct Count {
+    float2 n = make_float2(0.f, 0.f);
+  };
+  static __device__ __forceinline__ float one_above(unsigned x, float t) {
+    float d;
+    asm("set.gt.f32.f32 %0, %1, %2;" : "=f"(d) : "f"(__uint_as_float(x)), "f"(t));
+    return d;
+  }
   static __device__ __forceinline__ void above(Count &n, const uint4 &c, float t) {
-    n += (__uint_as_float(c.x) > t) + (__uint_as_float(c.y) > t) + (__uint_as_float(c.z) > t) + (__uint_as_float(c.w) > t);
+    n.n = __fadd2_rn(n.n, make_float2(one_above(c.x, t), one_above(c.y, t)));
+    n.n = __fadd2_rn(n.n, make_float2(one_above(c.z, t), one_above(c.w, t)));
   }
-  static __device__ __forceinline__ int total(Count n) { return n; }
-  static __device__ __forceinline__ float largest(const uint4 &c) {
-    return fmaxf(fmaxf(__uint_as_float(c.x), __uint_as_float(c.y)), fmaxf(__uint_as_float(c.z), __uint_as_float(c.w)));
-  }
+  static __device__ __forceinline__ int total(const Count &n) { return static_cast<int>(n.n.x + n.n.y); }
 };
 template <>
 struct Entries<__nv_bfloat16> {
@@ -161,10 +175,6 @@ struct Entries<__nv_bfloat16> {
   static __device__ __forceinline__ int total(const Count &n) {
     const float2 f = __bfloat1622float2(n.n);
     return static_cast<int>(f.x + f.y);
-  }
-  static __device__ __forceinline__ float largest(const uint4 &c) {
-    const float2 a = __bfloat1622float2(__hmax2(__hmax2(two(c.x), two(c.y)), __hmax2(two(c.z), two(c.w))));
-    return fmaxf(a.x, a.y);
   }
 };
 
@@ -264,48 +274,61 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas)
   // The rows with a token go round the clusters: cluster y has those whose number among them is y modulo
   // gridDim.y.  Warp 0 walks them ahead of the others and asks for their blocks; found[] holds the rows
   // it has come to and that are not done with.
-  int64_t scan = 0, ahead = -1;    // rows before `scan` have been walked; the row whose blocks are asked for
+  int64_t scan = 0;                // rows before it have been walked
   int wanted = blockIdx.y;         // number, counted from `scan`, of this cluster's next row with a token
-  int ahead_block = 0, issued = 0, taken = 0;  // blocks asked for and used
+  const uint4 *ahead = nullptr;    // chunks of the row last found that have not been asked for
+  int ahead_left = 0;
+  bool end = false;
+  int issued = 0, taken = 0;       // blocks asked for and used
   int listed = 0, done = 0;        // rows found and done with
-  auto next_row = [&]() -> int64_t {
+  auto next_row = [&] {
     while (scan < R) {
-      const int t = scan + lane < R ? tokens[scan + lane] : -1;
-      const unsigned live = __ballot_sync(0xffffffffu, t >= 0 && t < V);
-      const unsigned it = __ballot_sync(0xffffffffu, (live >> lane & 1u) && __popc(live & ((1u << lane) - 1u)) == wanted);
-      if (it) {
-        const int64_t row = scan + __ffs(it) - 1;
+      int t[kLpWalk];  // tokens of the rows ahead, on their way at once
+#pragma unroll
+      for (int u = 0; u < kLpWalk; ++u) t[u] = scan + u * 32 + lane < R ? __ldg(tokens + scan + u * 32 + lane) : -1;
+#pragma unroll
+      for (int u = 0; u < kLpWalk; ++u) {
+        if (scan + u * 32 >= R) break;
+        const bool has = t[u] >= 0 && t[u] < V;
+        const unsigned live = __ballot_sync(0xffffffffu, has);
+        if (wanted >= __popc(live)) {
+          wanted -= __popc(live);
+          continue;
+        }
+        const unsigned it = __ballot_sync(0xffffffffu, has && __popc(live & ((1u << lane) - 1u)) == wanted);
+        const int64_t row = scan + u * 32 + __ffs(it) - 1;
+        if (it >> lane & 1u) {
+          sh.found[listed % kLpRows] = row;
+          sh.token[listed % kLpRows] = t[u];
+        }
+        const RowPlace<Tin> p(logits + row * stride, V, C, part);
+        ahead = reinterpret_cast<const uint4 *>(p.x + p.head) + p.c0;
+        ahead_left = p.c1 - p.c0;
         scan = row + 1;
         wanted = gridDim.y - 1;
-        return row;
+        return;
       }
-      wanted -= __popc(live);
-      scan += 32;
+      scan += 32 * kLpWalk;
     }
-    return R;
+    if (lane == 0) sh.found[listed % kLpRows] = R;
+    end = true;
   };
   auto fill = [&] {  // warp 0: blocks for the stages that are free
     while (issued - taken < kLpStages) {
-      if (ahead >= 0) {
-        if (ahead == R) return;
-        const RowPlace<Tin> p(logits + ahead * stride, V, C, part);
-        if (ahead_block < p.blocks()) {
-          if (lane == 0) {
-            const int c = p.c0 + ahead_block * kLpChunks;
-            const uint32_t bytes = 16u * min(kLpChunks, p.c1 - c);
-            const int st = issued % kLpStages;
-            mbar_arrive_expect_tx(&sh.full[st], bytes);
-            bulk_load(stages + st * kLpStageBytes, reinterpret_cast<const uint4 *>(p.x + p.head) + c, bytes, &sh.full[st]);
-          }
-          ++issued;
-          ++ahead_block;
-          continue;
+      if (ahead_left > 0) {
+        const int n = min(kLpChunks, ahead_left);
+        if (lane == 0) {
+          const int st = issued % kLpStages;
+          mbar_arrive_expect_tx(&sh.full[st], 16u * n);
+          bulk_load(stages + st * kLpStageBytes, ahead, 16u * n, &sh.full[st]);
         }
+        ++issued;
+        ahead += n;
+        ahead_left -= n;
+        continue;
       }
-      if (listed - done == kLpRows) return;  // parts without blocks ask for none: rows are listed all the same
-      ahead = next_row();
-      ahead_block = 0;
-      if (lane == 0) sh.found[listed % kLpRows] = ahead;
+      if (end || listed - done == kLpRows) return;  // parts without blocks ask for none: rows are listed all the same
+      next_row();
       ++listed;
     }
   };
@@ -314,7 +337,7 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas)
     __syncthreads();
     const int64_t row = sh.found[done % kLpRows];
     if (row == R) break;  // (the whole cluster comes to the same end)
-    const int tok = tokens[row];
+    const int tok = sh.token[done % kLpRows];
     const RowPlace<Tin> at(logits + row * stride, V, C, part);
     const Tin *x0 = at.x;
     const int head = at.head, tail = at.tail, c0 = at.c0, c1 = at.c1;
@@ -334,71 +357,111 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas)
     me.z = me.w = 0.f;
     me.before = 0;
     me.none = 0;
+    bool exactly = false;     // how the thread's terms are summed
     float floor = -INFINITY;  // value that an alternative of this CTA has at least
-    for (int base = c0; base < c1 || base == c0; base += kLpChunks) {
-      uint4 x[kLpLoads];
-      const unsigned char *st = stages + taken % kLpStages * kLpStageBytes;
-      if (base < c1) {
-        if (!mbar_wait(&sh.full[taken % kLpStages], (taken / kLpStages) & 1u)) sh.gave_up = 1;
-      }
+    const float ex = edge >= 0 ? to_f32(x0[edge]) : -INFINITY;
+    for (int span = c0; span < c1 || span == c0; span += kLpSpan * kLpChunks) {
+      float span_top = -INFINITY;
+      int nb = 0;
+      for (int base = span; nb < kLpSpan && (base < c1 || base == c0); base += kLpChunks, ++nb) {
+        uint4 x[kLpLoads];
+        const unsigned char *st = stages + taken % kLpStages * kLpStageBytes;
+        if (base < c1) {
+          if (!mbar_wait(&sh.full[taken % kLpStages], (taken / kLpStages) & 1u)) sh.gave_up = 1;
+        }
+        auto chunk = [&](int i) {
+          return base + i * kLpThreads + tid < c1 ? *reinterpret_cast<const uint4 *>(st + (i * kLpThreads + tid) * 16) : En::none();
+        };
 #pragma unroll
-      for (int i = 0; i < kLpLoads; ++i)
-        x[i] = base + i * kLpThreads + tid < c1 ? *reinterpret_cast<const uint4 *>(st + (i * kLpThreads + tid) * 16) : En::none();
-      const float ex = (edge >= 0 && base == c0) ? to_f32(x0[edge]) : -INFINITY;
-      const float inner = En::largest_nan(x), top = fmax3_nan(inner, ex, ex);
-      me.none |= !(top < INFINITY);
-      // ---- sums, relative to the thread's own maximum
-      if (top > me.m) {
-        const float d = (me.m - top) * kLog2e, e = ex2(d);  // -inf and 0 at first: nothing is there yet
-        me.w = e > 0.f ? (me.w + me.z * d) * e : 0.f;
-        me.z *= e;
-        me.m = top;
-      }
-      const float mu = me.m == -INFINITY ? 0.f : me.m;
-      const float2 nm = make_float2(-mu, -mu), l2 = make_float2(kLog2e, kLog2e);
-      float2 z = make_float2(0.f, 0.f), w = make_float2(0.f, 0.f);
-      auto add = [&](float2 v) {
-        float2 y = __fmul2_rn(__fadd2_rn(v, nm), l2);
-        y.x = fmaxf(y.x, -300.f);  // 2^y is 0 there, and so is the product with it
-        y.y = fmaxf(y.y, -300.f);
-        const float2 p = make_float2(ex2(y.x), ex2(y.y));
-        z = __fadd2_rn(z, p);
-        w = __ffma2_rn(p, y, w);
-      };
+        for (int i = 0; i < kLpLoads; ++i) x[i] = chunk(i);
+        const float inner = En::largest_nan(x), extra = base == c0 ? ex : -INFINITY, top = fmax3_nan(inner, extra, extra);
+        sh.top[nb][tid] = __float2bfloat16_ru(inner);
+        span_top = fmaxf(span_top, top);
+        me.none |= !(top < INFINITY);
+        // ---- sums, relative to the thread's own maximum
+        if (top > me.m) {
+          const float d = (me.m - top) * kLog2e, e = ex2(d);  // -inf and 0 at first: nothing is there yet
+          me.w = e > 0.f ? (me.w + me.z * d) * e : 0.f;
+          me.z *= e;
+          me.m = top;
+        }
+        const float mu = me.m == -INFINITY ? 0.f : me.m;
+        float2 z = make_float2(0.f, 0.f), w = make_float2(0.f, 0.f);
+        auto add = [&](float2 y) {
+          const float2 p = make_float2(ex2(y.x), ex2(y.y));
+          z = __fadd2_rn(z, p);
+          w = __ffma2_rn(p, y, w);
+        };
+        const float2 l2 = make_float2(kLog2e, kLog2e);
+        // y of a pair in two steps, at least -300: 2^y is 0 there, and so is the product with it
+        auto add_exactly = [&](float2 v) {
+          const float2 y = __fmul2_rn(__fadd2_rn(v, make_float2(-mu, -mu)), l2);
+          add(make_float2(fmaxf(y.x, -300.f), fmaxf(y.y, -300.f)));
+        };
+        if (!exactly) {
+          // y in one step, v log2(e) - c with c = m log2(e) rounded: all terms off by the same
+          // r = m log2(e) - c, which the sums are rid of at the end
+          const float c = mu * kLog2e, r = fmaf(mu, kLog2e, -c), e = ex2(-r);
+          const float2 nc = make_float2(-c, -c);
 #pragma unroll
-      for (int i = 0; i < kLpLoads; ++i)
+          for (int i = 0; i < kLpLoads; ++i)
+            if (base + i * kLpThreads + tid < c1) {
 #pragma unroll
-        for (int e = 0; e < VE / 2; ++e) add(En::pair(x[i], e));
-      // ---- entries before the token
-      const int first = base + tid;
-      if (xt > -INFINITY) {
-        typename En::Count n{};
+              for (int j = 0; j < VE / 2; ++j) add(__ffma2_rn(En::pair(x[i], j), l2, nc));
+            }
+          w = __fmul2_rn(__ffma2_rn(z, make_float2(-r, -r), w), make_float2(e, e));
+          z = __fmul2_rn(z, make_float2(e, e));
+          // -inf, or what a product with log2(e) leaves of a value near the largest: its y of -inf has made
+          // w a NaN.  The block is summed again, and the row's later ones at once, in the two steps.
+          exactly = !(fabsf(w.x + w.y) < INFINITY);
+          if (exactly) z = w = make_float2(0.f, 0.f);
+        }
+        if (exactly) {
+#pragma unroll 1
+          for (int i = 0; i < kLpLoads; ++i) {
+            const uint4 xi = chunk(i);
 #pragma unroll
-        for (int i = 0; i < kLpLoads; ++i) En::above(n, x[i], first + i * kLpThreads < tok_after ? xt_before : xt);
-        me.before += En::total(n);
-      } else {  // nothing is below: above it are the finite ones, and with a lower index every entry
-        for (int i = 0; i < kLpLoads; ++i) {
+            for (int j = 0; j < VE / 2; ++j) add_exactly(En::pair(xi, j));
+          }
+        }
+        // ---- entries before the token
+        const int first = base + tid;
+        if (xt > -INFINITY && inner >= xt) {
           typename En::Count n{};
-          En::above(n, x[i], xt);
-          const int c = first + i * kLpThreads;
-          me.before += c < tok_after && c < c1 ? VE : En::total(n);
+#pragma unroll
+          for (int i = 0; i < kLpLoads; ++i) En::above(n, x[i], first + i * kLpThreads < tok_after ? xt_before : xt);
+          me.before += En::total(n);
+        } else if (xt == -INFINITY) {  // nothing is below: above it are the finite ones, and with a lower index every entry
+#pragma unroll 1
+          for (int i = 0; i < kLpLoads; ++i) {
+            typename En::Count n{};
+            En::above(n, chunk(i), xt);
+            const int c = first + i * kLpThreads;
+            me.before += c < tok_after && c < c1 ? VE : En::total(n);
+          }
+        }
+        if (tok_chunk >= base && tok_chunk < base + kLpChunks && (tok_chunk - base) % kLpThreads == tid)
+          for (int j = head + tok_chunk * VE; j < tok; ++j)  // of the token's own chunk, equal entries before it
+            me.before += to_f32(x0[j]) == xt;
+        if (edge >= 0 && base == c0) {
+          add_exactly(make_float2(ex, -INFINITY));
+          me.before += ex > xt || (ex == xt && edge < tok);
+        }
+        me.z += z.x + z.y;
+        me.w += w.x + w.y;
+        __syncthreads();  // this block's stage is done with
+        if (base < c1) {
+          ++taken;
+          if (warp == 0) fill();
         }
       }
-      if (tok_chunk >= base && tok_chunk < base + kLpChunks && (tok_chunk - base) % kLpThreads == tid)
-        for (int j = head + tok_chunk * VE; j < tok; ++j)  // of the token's own chunk, equal entries before it
-          me.before += to_f32(x0[j]) == xt;
-      if (edge >= 0 && base == c0) {
-        add(make_float2(ex, -INFINITY));
-        me.before += ex > xt || (ex == xt && edge < tok);
-      }
-      me.z += z.x + z.y;
-      me.w += w.x + w.y;
-      // ---- alternatives
-      if (K > 0 && base == c0) {  // the bound that the first block gives
-        float g = top;
+      if (K > 0) {
+        // ---- alternatives of the span: the bound
+        float g = span_top;
 #pragma unroll
         for (int o = 1; o < kPerGroup; o <<= 1) g = fmaxf(g, __shfl_xor_sync(0xffffffffu, g, o));
         if (tid % kPerGroup == 0) sh.group[tid / kPerGroup] = g;
+        if (tid == 0) sh.hits = 0;
         __syncthreads();
         if (tid < kLpGroups) {
           const float mine = sh.group[tid];
@@ -408,81 +471,93 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas)
           if (place == K - 1) sh.floor = mine;
         }
         __syncthreads();
-        floor = sh.floor;
-      }
-      int grown = 0;
-      if (K > 0 && top >= floor && top > -INFINITY) {  // few threads: their few chunks with such an entry
-        unsigned which = 0;
-#pragma unroll
-        for (int i = 0; i < kLpLoads; ++i) which |= static_cast<unsigned>(En::largest(x[i]) >= floor) << i;
+        floor = fmaxf(floor, sh.floor);
         auto aside = [&](float v, int j) {
           if (!(v >= floor) || v == -INFINITY) return;
           const int n = atomicAdd(&sh.count, 1);
           if (n < kLpList) sh.list[n] = order_key(v, j);
-          grown |= n >= kLpCut;
         };
-        for (; which; which &= which - 1) {
-          const int c = first + (__ffs(which) - 1) * kLpThreads;
-          if (c >= c1) break;
-          const Tin *chunk = reinterpret_cast<const Tin *>(st + (c - base) * 16);
-          const uint4 again = *reinterpret_cast<const uint4 *>(chunk);
-          unsigned those = 0;
+        // ---- the parts of blocks with an entry at or above it
+        if (span_top >= floor) {
+          for (int i = 0; i < nb; ++i) {
+            const float t = __bfloat162float(sh.top[i][tid]);
+            if (t >= floor && t > -INFINITY) {
+              const int n = atomicAdd(&sh.hits, 1);
+              if (n < kLpHits) sh.hit[n] = static_cast<unsigned short>(i * kLpThreads + tid);
+            }
+          }
+          if (span == c0 && edge >= 0) aside(ex, edge);
+        }
+        __syncthreads();
+        // ---- a warp takes such a part: four bytes a lane, four parts on their way at once
+        const int hits = sh.hits;
+        for (int h = warp; h < min(hits, kLpHits); h += 4 * (kLpThreads / 32)) {
+          unsigned word[4];
+          int at_entry[4];
 #pragma unroll
-          for (int e = 0; e < VE; ++e) {
-            const float2 v = En::pair(again, e / 2);
-            those |= static_cast<unsigned>((e % 2 ? v.y : v.x) >= floor) << e;
+          for (int u = 0; u < 4; ++u) {
+            const int hu = h + u * (kLpThreads / 32);
+            at_entry[u] = -1;
+            if (hu < min(hits, kLpHits)) {
+              const int hit = sh.hit[hu];
+              const int c = span + hit / kLpThreads * kLpChunks + (lane >> 2) * kLpThreads + hit % kLpThreads;
+              if (c < c1) {
+                at_entry[u] = head + c * VE + (lane & 3) * (VE / 4);
+                word[u] = *reinterpret_cast<const unsigned *>(x0 + at_entry[u]);
+              }
+            }
           }
-          for (; those; those &= those - 1) {  // mostly one
-            const int e = __ffs(those) - 1;
-            aside(to_f32(chunk[e]), head + c * VE + e);
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            if (at_entry[u] < 0) continue;
+            if constexpr (VE == 4) {
+              aside(__uint_as_float(word[u]), at_entry[u]);
+            } else {
+              aside(__uint_as_float(word[u] << 16), at_entry[u]);
+              aside(__uint_as_float(word[u] & 0xFFFF0000u), at_entry[u] + 1);
+            }
           }
         }
-        if (edge >= 0 && base == c0) aside(ex, edge);
-      }
-      grown = __syncthreads_or(grown);  // this block's stage and list are done with
-      if (base < c1) {
-        ++taken;
-        if (warp == 0) fill();
-      }
-      if (!grown) continue;
-      if (sh.count > kLpList) {
-        // more than the list holds: the largest key below the last one, K times, of this block and of what
-        // the list had before it (entries of this block that are in the list count once: keys are unique)
-        unsigned long long last = ~0ull;
-        for (int k = 0; k < K; ++k) {
-          unsigned long long b = 0;
-          auto see = [&](unsigned long long key) {
-            if (key < last && key > b) b = key;
-          };
-          for (int i = tid; i < kLpList; i += kLpThreads) see(sh.list[i]);
-          const int e1 = head + min(base + kLpChunks, c1) * VE;
-          for (int j = head + base * VE + tid; j < e1; j += kLpThreads) {
-            const float v = to_f32(x0[j]);
-            if (v > -INFINITY) see(order_key(v, j));
+        __syncthreads();
+        if (hits > kLpHits || sh.count > kLpList) {
+          // more than the lists hold: the largest key below the last one, K times, of this span and of what
+          // the list had before it (entries of this span that are in the list count once: keys are unique)
+          unsigned long long last = ~0ull;
+          for (int k = 0; k < K; ++k) {
+            unsigned long long b = 0;
+            auto see = [&](unsigned long long key) {
+              if (key < last && key > b) b = key;
+            };
+            for (int i = tid; i < min(sh.count, kLpList); i += kLpThreads) see(sh.list[i]);
+            const int e1 = head + min(span + kLpSpan * kLpChunks, c1) * VE;
+            for (int j = head + span * VE + tid; j < e1; j += kLpThreads) {
+              const float v = to_f32(x0[j]);
+              if (v > -INFINITY) see(order_key(v, j));
+            }
+            if (edge >= 0 && span == c0 && ex > -INFINITY) see(order_key(ex, edge));
+            for (int o = 16; o; o >>= 1) {
+              const unsigned long long y = __shfl_xor_sync(0xffffffffu, b, o);
+              b = y > b ? y : b;
+            }
+            if (lane == 0) sh.red[warp] = b;
+            __syncthreads();
+            b = 0;
+            for (int i = 0; i < kLpThreads / 32; ++i) b = sh.red[i] > b ? sh.red[i] : b;
+            if (tid == 0) sh.best[k] = b;
+            last = b;
+            __syncthreads();
           }
-          if (edge >= 0 && base == c0 && ex > -INFINITY) see(order_key(ex, edge));
-          for (int o = 16; o; o >>= 1) {
-            const unsigned long long y = __shfl_xor_sync(0xffffffffu, b, o);
-            b = y > b ? y : b;
-          }
-          if (lane == 0) sh.red[warp] = b;
-          __syncthreads();
-          b = 0;
-          for (int i = 0; i < kLpThreads / 32; ++i) b = sh.red[i] > b ? sh.red[i] : b;
-          if (tid == 0) sh.best[k] = b;
-          last = b;
+        } else {
+          put_in_order(sh.list, sh.count, sh.best, K);
+        }
+        if (span + kLpSpan * kLpChunks < c1) {  // the best K are the list now
+          if (tid < K) sh.list[tid] = sh.best[tid];
+          if (tid == 0) sh.count = K;
+          if (sh.best[K - 1] != 0) floor = fmaxf(floor, key_value(sh.best[K - 1]));
           __syncthreads();
         }
-      } else {
-        put_in_order(sh.list, sh.count, sh.best, K);
       }
-      // the best K are the list now
-      if (tid < K) sh.list[tid] = sh.best[tid];
-      if (tid == 0) sh.count = K;
-      if (sh.best[K - 1] != 0) floor = fmaxf(floor, key_value(sh.best[K - 1]));
-      __syncthreads();
     }
-    if (K > 0) put_in_order(sh.list, sh.count, sh.best, K);
     // ---- this CTA's part
     warp_fold(me);
     if (lane == 0) sh.warp[warp] = me;

@@ -186,3 +186,38 @@ def test_scores_a_round_and_replays():
         graph.replay()
         assert mgd.mgd_workspace_errors(ws) == 0
         _check(t, tok, 3, out)
+
+
+def test_many_long_rows_of_every_pattern():
+    """More rows than fit at once, each longer than what its alternatives are chosen from in one go: ties,
+    sorted and masked rows, and rows without a token among them."""
+    dev = gpu_or_skip()
+    V, R, K = 70001, 480, 32
+    rows = [x for _, x in _patterns(V, dev)]
+    x = torch.stack([rows[i % len(rows)].roll(i) for i in range(R)])
+    x[::7] = torch.randn((len(range(0, R, 7)), V), device=dev)
+    tok = torch.randint(0, V, (R,), device=dev).to(torch.int32)
+    tok[3::11] = -1
+    out, err = _run(x, tok, K)
+    assert err == 0
+    few = [*range(0, 36), *range(R - 12, R)]
+    _check(x[few], tok[few], K, {n: t[few] for n, t in out.items()})
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+def test_rows_far_from_zero(dtype):
+    """Large common offsets and sizes: the entries' differences from the maximum are what counts."""
+    dev = gpu_or_skip()
+    V, K = 20000, 8
+    g = torch.Generator(device=dev).manual_seed(5)
+    base = 3 * torch.randn((10, V), generator=g, device=dev)
+    for i, (add, times) in enumerate([(100, 1), (-100, 1), (1e4, 1), (-1e4, 1), (1e6, 1), (-3e9, 1), (0, 1e4), (0, -1e9),
+                                      (0, 1e36), (1e37, 1e30)]):
+        base[i] = add + base[i] * times
+    x = base.to(dtype)
+    x[:5, ::3] = -math.inf
+    tok = x.float().argmax(-1).to(torch.int32)
+    tok[1::2] = 7
+    out, err = _run(x, tok, K)
+    assert err == 0
+    _check(x, tok, K, out)

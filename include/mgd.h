@@ -459,6 +459,7 @@ mgd_status mgd_prefix_attn(const void *q, const void *k_prefix, const void *v_pr
  *             e.g. the length of a shared prefix)
  *   q_out     [B, T, Hq, D] dtype, contiguous (may be q itself when q is)
  *   k, v      [B, Hkv, kv_cap, D] dtype, strides as for mgd_verify_attn
+ * Outputs overlap neither each other nor an input, but for q_out == q.
  *
  * New row t < n_b goes to cache row kv_len[b] - n_b + t; its position is that
  * row plus the offset.  Elements i and i + rotary_dim/2 of a head (interleaved

@@ -269,6 +269,14 @@ def _as_wanted(device, dense, int32, f32, same):
     return True
 
 
+def _on_current(device):
+    """The launch goes to the current device: refuse tensors of another one, or of the host."""
+    if device.index is None:
+        raise ValueError("the tensors are on %s: a CUDA device is needed" % device)
+    if device.index != torch.cuda.current_device():
+        raise ValueError("the tensors are on %s, the current device is cuda:%d" % (device, torch.cuda.current_device()))
+
+
 def prefix_attn(q, k_prefix, v_prefix, prefix_len, k, v, kv_len, sm_scale=None, out_dtype=torch.float32, ws=None,
                 out=None, lse=None, stream=None):
     """Verify (T = 1: draft) attention of a batch over a prefix that all its sequences share and each
@@ -304,6 +312,7 @@ def prefix_attn(q, k_prefix, v_prefix, prefix_len, k, v, kv_len, sm_scale=None, 
                same=[("q", q), ("k_prefix", k_prefix), ("v_prefix", v_prefix), ("k", k), ("v", v)])
     if ws is None:
         ws = workspace(mgd.mgd_prefix_workspace_size(B, T, Hq, Hkv, D, pshape[1], cap), dev)
+    _on_current(dev)
     mgd.mgd_prefix_attn(q, k_prefix, v_prefix, prefix_len, pshape[1], ps[0], k, v, kv_len, B, T, Hq, Hkv, D, cap, sb, sh,
                         scale, _dtype_code(q), out, _dtype_code(out), lse, ws, ws.numel(), stream)
     return out, lse
@@ -385,6 +394,7 @@ def rope_append(q, k_new, v_new, table, k, v, kv_len, new_len=None, pos_offset=N
                same=[("q", q), ("k_new", k_new), ("v_new", v_new), ("k", k), ("v", v), ("q_out", q_out)])
     if ws is None:
         ws = workspace(mgd.mgd_rope_workspace_size(B), dev)
+    _on_current(dev)
     mgd.mgd_rope_append(q, sq, k_new, sk, v_new, sv, turns, table.magnitude, table.rotary_dim, int(interleaved), B, T, Hq,
                         Hkv, D, _dtype_code(q), kv_len, new_len, pos_offset, 1 if offsets > 1 else 0, q_out, k, v, cap, sb,
                         sh, ws, ws.numel(), stream)
@@ -427,6 +437,8 @@ def token_logprobs(logits, tokens, top=0, ws=None, out=None, stream=None):
         _check(dev, dense=ints + floats, int32=ints, f32=floats)
     if ws is None:
         ws = workspace(mgd.mgd_logprobs_workspace_size(R, V, top), dev)
-    mgd.mgd_token_logprobs(logits, step or V, _dtype_code(logits), tokens, R, V, top, logprob, entropy, rank, ids, lps, ws,
+    code = _dtype_code(logits)
+    _on_current(dev)
+    mgd.mgd_token_logprobs(logits, step or V, code, tokens, R, V, top, logprob, entropy, rank, ids, lps, ws,
                            ws.numel(), stream)
     return out

@@ -102,3 +102,20 @@ def test_two_rounds_behind_a_shared_prefix(captured):
                 assert abs(float(lp["logprob"][b, t]) - e[0]) <= 2e-5 + 2.0 ** -22 * abs(e[0])
                 assert int(lp["rank"][b, t]) == e[2] and lp["top_ids"][b, t].tolist() == e[3]
         assert kv_len.tolist() == [int(before[b]) + 1 + n[b] for b in range(B)]
+
+
+def test_tensors_of_another_device_are_refused(monkeypatch):
+    dev = gpu_or_skip()
+    x = torch.zeros((2, 8), device=dev)
+    tok = torch.zeros(2, dtype=torch.int32, device=dev)
+    i32 = torch.ones(2, dtype=torch.int32, device=dev)
+    q = torch.zeros((2, 1, 4, 64), device=dev)
+    kv = torch.zeros((2, 2, 8, 64), device=dev)
+    table = ops.rope_table(64, device=dev)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
+    with pytest.raises(ValueError, match="current device"):
+        ops.token_logprobs(x, tok)
+    with pytest.raises(ValueError, match="current device"):
+        ops.rope_append(q, q[:, :, :2].contiguous(), q[:, :, 2:].contiguous(), table, kv, kv.clone(), i32)
+    with pytest.raises(ValueError, match="current device"):
+        ops.prefix_attn(q, kv[0], kv[1], i32[:1], kv, kv, i32)

@@ -191,3 +191,12 @@ def test_logprobs_wrapper_refuses_what_the_pointers_would_hide():
                top_ids=torch.zeros((2, 3, 4), dtype=torch.int32), top_logprobs=torch.zeros(2, 3, 4))
     with pytest.raises(ValueError, match="top_ids"):
         ops.token_logprobs(x, tok, top=5, out=out)
+
+
+def test_host_tensors_are_refused():
+    x, tok = torch.zeros((2, 8)), torch.zeros(2, dtype=torch.int32)
+    with pytest.raises(ValueError, match="CUDA device"):
+        ops.token_logprobs(x, tok)
+    a = _prefix_args()
+    with pytest.raises(ValueError, match="CUDA device"):
+        ops.prefix_attn(**a)

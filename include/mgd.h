@@ -428,7 +428,8 @@ mgd_status mgd_spec_sample_noalloc(const float *target_logits, const float *draf
  * 0 .. kv_len[b]-T+t; scores are sm_scale * <q, k>; softmax and accumulation in
  * float32.  With bf16 inputs the probabilities over the prefix enter the P V
  * product as float16 with V converted to float16 (11 significant bits): |v| <=
- * 65504 is needed as in mgd_verify_attn's float16 form.
+ * 65504 is needed as in mgd_verify_attn's float16 form, and entries below 2^-14
+ * keep an absolute accuracy of 2^-25.
  * A prefix_len out of range leaves every output unspecified, a kv_len out of
  * range that sequence's (MGD_DEVERR_KV_LEN).
  * Supported: D in {64, 128}; 1 <= T <= 17; Hq % Hkv == 0; fewer than 2^31 rows

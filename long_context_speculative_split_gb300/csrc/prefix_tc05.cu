@@ -20,15 +20,18 @@
 // P in float16 has 11 significant bits (bfloat16: 8), which keeps the error of the
 // P V product at 1.5e-4 of the result; an MMA takes A and B of one type, so four
 // warps convert the V tiles in place once they have landed (exact for magnitudes in
-// [2^-14, 65504]).  m_w is not the running maximum: it starts 2^4 above a row's first
-// maximum and is raised when a score exceeds it by more than 2^14 (P stays within
-// float16's 2^16, and is at least 2^-4 at the maximum, 2^10 above the subnormals), which
-// means rescaling O_w in tensor memory.  The sum of exponentials is kept in float32,
-// unrounded.
+// [2^-14, 65504]).  m_w is not the running maximum: it is a row's first maximum, raised when a
+// score exceeds it by more than 2^15 (P stays within float16's 2^16), which means rescaling O_w in
+// tensor memory.  Weights below 2^-14 of the maximum come in steps of 2^-24 of it, as they
+// would against the running maximum; starting m_w above the first maximum, for fewer raises, would
+// lose as much at that end (640 rows on 32768 keys, 1 % of them large: 320 us from the first
+// maximum, 325 us from 2^4 above it and without raises 306 us).  The sum of exponentials is
+// kept in float32, unrounded.
 //
 // Roles (16 warps a CTA): 0-3 and 4-7 softmax of slot 0 / 1, 8-11 V's conversion,
-// 12 and 13 MMA issue for slot 0 / 1 (of the first CTA), 14 query rows, K and V tiles by TMA.  Registers a thread: 184, 88 and 56
-// for the three kinds of warp group (2 * 184 + 88 + 56 = 4 * 128, the launch's own total).
+// 12 and 13 MMA issue for slot 0 / 1 (of the first CTA), 14 query rows, K and V tiles by TMA.
+// Registers a thread: 184, 88 and 56 for the three kinds of warp group (2 * 184 + 88 + 56 =
+// 4 * 128, the launch's own total).
 #include <algorithm>
 #include <type_traits>
 
@@ -43,8 +46,8 @@ constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kPRows = 128;   // query rows of a slot in one CTA
 constexpr int kPKeys = 128;   // keys of a tile
 constexpr int kPThreads = 512;
-// P = 2^(score - m): m starts 2^kHead above a row's first maximum and follows it once it is 2^kRaise above m.
-constexpr float kRaise = 14.f, kHead = 4.f;
+// P = 2^(score - m): m starts at a row's first maximum and follows it once it is 2^kRaise above m.
+constexpr float kRaise = 15.f;
 
 template <int D>
 struct PLayout {
@@ -260,8 +263,8 @@ __device__ __forceinline__ bool all_wait(uint64_t *bar, uint32_t parity, WsHeade
 }
 
 // One row's scores of a group of 64 keys: P = 2^(s * sl2 - m) over S as float16 pairs, its float32 sum
-// added to l.  A maximum that exceeds the row's m by more than 2^kRaise raises m first (to the maximum
-// and 2^kHead); `settle` waits until the products issued so far are done, so that O can be rescaled.
+// added to l.  A maximum that exceeds the row's m by more than 2^kRaise raises m to it
+// first; `settle` waits until the products issued so far are done, so that O can be rescaled.
 // kMask: only the first nk keys count.  A template and not a branch within: the compiler would
 // predicate the selections into every group.
 template <int D, bool kMask, typename Settle>
@@ -287,7 +290,7 @@ __device__ __forceinline__ void softmax_group(uint32_t s_addr, uint32_t o_addr, 
   const float mt = top == -INFINITY ? -INFINITY : top * sl2;
   const bool raise = mt > m + kRaise || (m == -INFINITY && mt > -INFINITY);
   if (__any_sync(0xffffffffu, raise)) {
-    const float mn = raise ? mt + kHead : m;
+    const float mn = raise ? mt : m;
     const float alpha = raise ? ex2(m - mn) : 1.f;  // m == -inf: 0, nothing is there yet
     m = mn;
     l *= alpha;

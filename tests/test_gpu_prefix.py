@@ -273,3 +273,31 @@ def test_two_streams_with_their_own_workspaces():
     for (o, l), (ro, rl), w in zip(outs, serial, wss):
         assert mgd.mgd_workspace_errors(w) == 0
         assert torch.equal(o, ro) and torch.equal(l, rl)
+
+
+@pytest.mark.parametrize("gap", [8.0, 12.0, 14.5, 16.0])
+@pytest.mark.parametrize("late", [False, True], ids=["first", "last"])
+def test_many_small_weights_beside_a_large_one(gap, late):
+    """One prefix key outweighs each of 16383 others by e^gap, and the others' values agree, so that what they
+    add up to shows: 16383 e^-gap of the result.  A weight of the prefix is held in float16 relative to the
+    largest, in steps of 2^-24 below 2^-14: off by at most 2^-25, all in the same direction, so the sum of
+    their part is off by at most 16383 * 2^-25 = 4.9e-4 beside the attention calls' own 1e-3."""
+    dev = gpu_or_skip()
+    B, T, Hq, Hkv, D, P = 2, 2, 8, 2, 128, 16384
+    q = torch.zeros((B, T, Hq, D), device=dev)
+    q[..., 0] = 1.0
+    kp = torch.zeros((Hkv, P, D), device=dev)
+    kp[:, P - 1 if late else 0, 0] = gap
+    vp = torch.ones((Hkv, P, D), device=dev)
+    vp[:, P - 1 if late else 0] = 0.0
+    a = dict(q=q, k_prefix=kp, v_prefix=vp, k=torch.full((B, Hkv, 4, D), -1.0, device=dev),
+             v=torch.zeros((B, Hkv, 4, D), device=dev))
+    a = {n: x.to(torch.bfloat16) for n, x in a.items()}
+    a["k"][..., 0] = -50.0
+    a.update(prefix_len=torch.tensor([P], dtype=torch.int32, device=dev),
+             kv_len=torch.full((B,), 4, dtype=torch.int32, device=dev))
+    out, lse = ops.prefix_attn(**a, sm_scale=1.0)
+    ref, ref_lse = _reference(a, scale=1.0)
+    part = (P - 1) * math.exp(-gap) / (1 + (P - 1) * math.exp(-gap))
+    assert (out.double() - ref).abs().max() <= 4.9e-4 / (1 + (P - 1) * math.exp(-gap)) + 1e-3 * part
+    assert_lse_close(lse, ref_lse.cpu().numpy())

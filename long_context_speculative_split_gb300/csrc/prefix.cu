@@ -232,69 +232,81 @@ __global__ void __launch_bounds__(kMergeThreads)
                         const int32_t *__restrict__ prefix_len, const int32_t *__restrict__ kv_len, PrefixGeom g,
                         int grid, OwnChunks own, float *__restrict__ out_f32, __nv_bfloat16 *__restrict__ out_bf16, float *__restrict__ lse_out) {
   pdl_launch_dependents();
-  constexpr int kLanes = D / 4;
+  constexpr int kLanes = D / 4, kRows = kMergeThreads / kLanes;
+  static_assert(kSRows % kRows == 0, "a CTA's rows belong to one row block of the prefix");
   const int d = 4 * (threadIdx.x % kLanes);
-  const int64_t row = static_cast<int64_t>(blockIdx.x) * (kMergeThreads / kLanes) + threadIdx.x / kLanes;  // (b, t, hq)
   // The length and the places come before the wait: the kernels before this one let it start only after
   // their own wait for whatever wrote the call's inputs.
   const int plen = prefix_len[0];
-  const int bt = row >> 31 ? static_cast<int>(row / g.Hq) : static_cast<int>(row) / g.Hq;
-  const int hq = static_cast<int>(row - static_cast<int64_t>(bt) * g.Hq);
-  const int h = hq / g.G, gg = hq - h * g.G;
   const bool valid = plen >= 0 && plen <= g.prefix_cap;  // else: flagged by the prefix kernel
+  const int per_head = (g.R + kRows - 1) / kRows, h = blockIdx.x / per_head;
+  const int r0 = (blockIdx.x - h * per_head) * kRows, rt = r0 / g.tile_rows, r = r0 + threadIdx.x / kLanes;
   int c0 = 0, c1 = -1;
-  int64_t at0 = 0;
   if (valid && plen > 0) {
-    const int r = bt * g.G + gg;
-    const int rt = r / g.tile_rows, lr = r % g.tile_rows;
     const PrefixLine w = prefix_line(g, plen, grid);
     const int begin = prefix_pair_begin(w, h, rt);
     c0 = prefix_cta_of(w, begin);
     c1 = prefix_cta_of(w, begin + prefix_pair_steps(g, w, rt) - 1);
-    at0 = static_cast<int64_t>(h * g.RT + rt) * g.slot_rows + lr;
   }
+  const int64_t at0 = static_cast<int64_t>(h * g.RT + rt) * g.slot_rows + (r - rt * g.tile_rows);
+  const int bt = r / g.G, gg = r - bt * g.G;
+  const int64_t row = static_cast<int64_t>(bt) * g.Hq + h * g.G + gg;  // of the outputs: (b, t, hq)
   pdl_wait();
-  if (!valid || row >= static_cast<int64_t>(g.B) * g.T * g.Hq) return;
+  if (!valid || r >= g.R) return;
   float m = -INFINITY, sum = 1.f;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-  // one more partial result
-  auto add = [&](float l, const float4 &x) {
-    const float mn = fmaxf(m, l);
+  // kN more partial results, those from n on left out; their weights relative to the largest so far
+  constexpr int kN = 4;
+  auto add = [&](const float (&l)[kN], const float4 (&x)[kN], int n) {
+    float mn = m;
+#pragma unroll
+    for (int i = 0; i < kN; ++i)
+      if (i < n) mn = fmaxf(mn, l[i]);
     if (mn == -INFINITY) return;  // no finite score so far
-    const float a = expf(m - mn), b = expf(l - mn);
-    sum = sum * a + b;
-    o.x = o.x * a + x.x * b;
-    o.y = o.y * a + x.y * b;
-    o.z = o.z * a + x.z * b;
-    o.w = o.w * a + x.w * b;
+    const float a = ex2((m - mn) * kLog2e);
+    sum *= a;
+    o.x *= a;
+    o.y *= a;
+    o.z *= a;
+    o.w *= a;
+#pragma unroll
+    for (int i = 0; i < kN; ++i)
+      if (i < n) {
+        const float b = ex2((l[i] - mn) * kLog2e);
+        sum += b;
+        o.x = fmaf(x[i].x, b, o.x);
+        o.y = fmaf(x[i].y, b, o.y);
+        o.z = fmaf(x[i].z, b, o.z);
+        o.w = fmaf(x[i].w, b, o.w);
+      }
     m = mn;
+  };
+  // `n` of them at `at`, `at + step` ..., kN on their way at once
+  auto add_all = [&](const float *pl, const float *po, int64_t at, int64_t step, int n) {
+    for (int c = 0; c < n; c += kN) {
+      float l[kN];
+      float4 x[kN];
+#pragma unroll
+      for (int i = 0; i < kN; ++i)
+        if (c + i < n) {
+          l[i] = __ldcg(pl + at + (c + i) * step);
+          x[i] = __ldcg(reinterpret_cast<const float4 *>(po + (at + (c + i) * step) * D + d));
+        }
+      add(l, x, n - c);
+    }
   };
   if (own.count == 0) {  // one own result a row, in the rows' order
     m = __ldcg(own_l + row);
     o = __ldcg(reinterpret_cast<const float4 *>(own_o + row * D + d));
   } else {
-    const int b = bt / g.T, r = (bt - b * g.T) * g.G + gg;
+    const int b = bt / g.T, ro = r - b * g.T * g.G;  // row among the sequence's own
     const int n = min(own.count, (kv_len[b] + own.keys - 1) / own.keys);
-    const int64_t at = (static_cast<int64_t>(b * g.Hkv + h) * own.row_tiles + r / kSRows) * own.count * own.slot_rows + r % kSRows;
-    m = own_l[at];
-    o = *reinterpret_cast<const float4 *>(own_o + at * D + d);
-    for (int c = 1; c < n; ++c)
-      add(own_l[at + c * own.slot_rows], *reinterpret_cast<const float4 *>(own_o + (at + c * own.slot_rows) * D + d));
+    const int64_t at = (static_cast<int64_t>(b * g.Hkv + h) * own.row_tiles + ro / kSRows) * own.count * own.slot_rows + ro % kSRows;
+    m = __ldcg(own_l + at);
+    o = __ldcg(reinterpret_cast<const float4 *>(own_o + at * D + d));
+    add_all(own_l, own_o, at + own.slot_rows, own.slot_rows, n - 1);
   }
-  for (int c = c0; c <= c1; c += 4) {  // four partial results on their way at once
-    float l[4];
-    float4 x[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (c + i <= c1) {
-        const int64_t at = at0 + static_cast<int64_t>(c + i) * g.slot_rows;
-        l[i] = __ldcg(part_l + at);
-        x[i] = __ldcg(reinterpret_cast<const float4 *>(part_o + at * D + d));
-      }
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (c + i <= c1) add(l[i], x[i]);
-  }
+  add_all(part_l, part_o, at0 + static_cast<int64_t>(c0) * g.slot_rows, g.slot_rows, c1 - c0 + 1);
   const float inv = 1.f / sum;
   o.x *= inv;
   o.y *= inv;
@@ -337,9 +349,8 @@ cudaError_t launch_prefix_simt(const PrefixPlan &p, const PrefixArgs &a, const A
 
 cudaError_t launch_prefix_merge(const PrefixPlan &p, const PrefixArgs &a, const int32_t *kv_len) {
   const unsigned char *ws = static_cast<const unsigned char *>(a.ws);
-  const int64_t rows = static_cast<int64_t>(p.g.B) * p.g.T * p.g.Hq;
   const int per = kMergeThreads / (p.g.D / 4);
-  const dim3 grid(static_cast<unsigned>((rows + per - 1) / per));
+  const dim3 grid(static_cast<unsigned>((p.g.R + per - 1) / per) * p.g.Hkv);
   return launch_pdl(p.g.D == 128 ? prefix_merge_kernel<128> : prefix_merge_kernel<64>, grid, dim3(kMergeThreads), 0,
                     a.stream, reinterpret_cast<const float *>(ws + p.off_own_o),
                     reinterpret_cast<const float *>(ws + p.off_own_l),

@@ -222,7 +222,10 @@ __global__ void __launch_bounds__(kSThreads)
 
 // ---------------------------------------------------------------- merge
 // D / 4 lanes per query row, four columns each: the own part and the row's partial results over the
-// prefix, weighted by their log-sum-exps.  Bound by L2: own part, partial results and output once each.
+// prefix, weighted by their log-sum-exps.  A CTA's rows are of one head and one row block, so their places
+// are worked out once.  Bound by L2 and by latency: own part, partial results and output once each
+// (about 2 us for a few rows, 12 us for 20480 rows of 128 with two or three partial results; two or eight
+// of these on their way at once instead of four: 0.4 and 0.5 us more for 128 rows on 8192 keys).
 constexpr int kMergeThreads = 256;
 
 template <int D>

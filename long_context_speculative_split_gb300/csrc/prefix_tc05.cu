@@ -28,6 +28,11 @@
 // maximum, 325 us from 2^4 above it and without raises 306 us).  The sum of exponentials is
 // kept in float32, unrounded.
 //
+// Measured, 640 rows of 32 query and 8 KV heads of 128 on 32768 keys (344 GFLOP): 308 us on 60
+// clusters, 1.12 PFLOP/s, tensor pipe 63 % busy in their SMs; 171 key tiles a cluster at 1.8 us, of which
+// the MMAs are 1.15.  Bound by the chain S, softmax, P V of a slot, which the other group and slot cover
+// in part.
+//
 // Roles (16 warps a CTA): 0-3 and 4-7 softmax of slot 0 / 1, 8-11 V's conversion,
 // 12 and 13 MMA issue for slot 0 / 1 (of the first CTA), 14 query rows, K and V tiles by TMA.
 // Registers a thread: 184, 88 and 56 for the three kinds of warp group (2 * 184 + 88 + 56 =

@@ -565,8 +565,7 @@ mgd_status mgd_prefix_attn(const void *q, const void *k_prefix, const void *v_pr
   const bool q_tma =
       128 % G == 0 && sm_scale >= 0.f && encode_qwin_tensor_map(&pq, q, 1, B * T, Hq, D, G, 128 / G) == 0;
   plan.grid = prefix_share(plan, prefix_tc05_clusters(D, plan.grid), current_sm_count());
-  cudaError_t e = clear_attention_tickets(plan.own, ws, a.stream);
-  if (e == cudaSuccess) e = launch_prefix_tc05(plan, a, pk, pv, q_tma ? &pq : nullptr);
+  cudaError_t e = launch_prefix_tc05(plan, a, pk, pv, q_tma ? &pq : nullptr);
   if (e == cudaSuccess) e = launch_attention_beside(plan.own, o, km, vm);
   if (e == cudaSuccess) e = launch_prefix_merge(plan, a, kv_len);
   return e == cudaSuccess ? ok() : cuda_fail(e, "prefix attention launch");

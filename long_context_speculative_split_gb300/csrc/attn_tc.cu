@@ -33,7 +33,8 @@
 //     a partial (O, lse) and the CTA that completes the last chunk of that
 //     sequence merges all partials (atomic ticket, no waiting);
 //   * behind a shared prefix (kBeside) the kernel runs beside the prefix kernel, on the
-//     SMs that it leaves free, and only waits for it before it ends.
+//     SMs that it leaves free, and only waits for it before it ends; the partials of
+//     split sequences are joined by the kernel that joins them with the prefix's.
 #include <algorithm>
 
 #include "common.cuh"
@@ -482,7 +483,9 @@ __global__ void __launch_bounds__(kThreads, MINB)
       for (int e = 0; e < 2; ++e) f[j][e] = exp2f(m_run[j][e] - sm_rowM[8 * j + 2 * tig + e]);
 
     const int nch_b = (L + p.C - 1) / p.C;
-    const bool single = (nch_b == 1);
+    // beside the prefix kernel split sequences stay in parts: the kernel that joins prefix and own
+    // results joins them as well
+    const bool single = kBeside ? p.nchunk == 1 : nch_b == 1;
     const size_t part_base = (static_cast<size_t>(pair) * p.nchunk + chunk) * 32;
     // The 4 warps' scaled accumulators meet in kSlices slices of 8*NT rows (as many as the
     // 32-row buffer holds): the warps of round 0 store their slice, later rounds add into
@@ -555,7 +558,7 @@ __global__ void __launch_bounds__(kThreads, MINB)
       }
       named_bar(1, kConsumerWarps * 32);
     }
-    if (single) continue;
+    if (kBeside || single) continue;
 
     // ---- the CTA that finishes the last chunk of this pair merges all partials
     __threadfence();
@@ -688,19 +691,18 @@ cudaError_t launch_any(const AttnPlan &pl, const AttnArgs &a, const CUtensorMap 
 
 int attn_tc_min_blocks(int NT) { return NT <= 3 ? 2 : 1; }
 
-// The header needs no clearing launch: the kernel leaves it ready for the next call
-// (the workspace is zero-filled before its first use).  The merge tickets of split
-// sequences are cleared here, since a call of another shape may have written
-// partial results where this call keeps them.
-cudaError_t clear_attention_tickets(const AttnPlan &pl, void *ws, cudaStream_t stream) {
-  if (pl.nchunk <= 1) return cudaSuccess;
-  return cudaMemsetAsync(static_cast<unsigned char *>(ws) + pl.off_tickets, 0, pl.off_part_o - pl.off_tickets, stream);
-}
-
 cudaError_t launch_attention_tc(const AttnPlan &pl, const AttnArgs &a, const CUtensorMap &kmap,
                                 const CUtensorMap &vmap) {
-  cudaError_t e = clear_attention_tickets(pl, a.ws, a.stream);
-  return e != cudaSuccess ? e : launch_any<false>(pl, a, kmap, vmap);
+  // The header needs no clearing launch: the kernel leaves it ready for the next call
+  // (the workspace is zero-filled before its first use).  The merge tickets of split
+  // sequences are cleared here, since a call of another shape may have written
+  // partial results where this call keeps them.
+  if (pl.nchunk > 1) {
+    cudaError_t e = cudaMemsetAsync(static_cast<unsigned char *>(a.ws) + pl.off_tickets, 0,
+                                    pl.off_part_o - pl.off_tickets, a.stream);
+    if (e != cudaSuccess) return e;
+  }
+  return launch_any<false>(pl, a, kmap, vmap);
 }
 
 cudaError_t launch_attention_beside(const AttnPlan &pl, const AttnArgs &a, const CUtensorMap &kmap,
@@ -708,7 +710,7 @@ cudaError_t launch_attention_beside(const AttnPlan &pl, const AttnArgs &a, const
   return launch_any<true>(pl, a, kmap, vmap);
 }
 
-AttnPlan plan_attention(int B, int T, int Hq, int Hkv, int D, int kv_cap, int sm_count, bool whole) {
+AttnPlan plan_attention(int B, int T, int Hq, int Hkv, int D, int kv_cap, int sm_count, bool parts) {
   AttnPlan p{};
   p.B = B;
   p.T = T;
@@ -734,9 +736,14 @@ AttnPlan plan_attention(int B, int T, int Hq, int Hkv, int D, int kv_cap, int sm
   // 16k keys 0.215 -> 0.172 ms and 0.373 -> 0.320 ms).
   int C = 16384;
   const int cmin = std::max(256, ((kv_cap + 63) / 64 + 63) / 64 * 64);
-  // `whole`: the same for any number of pairs (the own caches behind a shared prefix, which are short).
-  if (p.pairs > slots && !whole)
+  if (p.pairs > slots && !parts)
     while (C > cmin && static_cast<long long>(p.pairs) * ((kv_cap + C - 1) / C) < 3LL * slots) C /= 2;
+  // `parts`: the own caches behind a shared prefix, beside whose kernel only some of the SMs are free
+  // and which are joined in parts by a kernel that runs anyway: a unit for every slot, of 512 keys or more
+  // (4 sequences of 8000 own keys behind 8192 shared ones: 46 us, 109 us whole; 32 of 512: 38 us whole,
+  // 42 us in halves).
+  if (parts)
+    while (C > std::max(cmin, 512) && static_cast<long long>(p.pairs) * ((kv_cap + C - 1) / C) < slots) C /= 2;
   if (C < cmin) C = cmin;
   p.C = C;
   p.nchunk = (kv_cap + C - 1) / C;

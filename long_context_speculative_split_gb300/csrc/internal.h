@@ -74,7 +74,7 @@ struct AttnPlan {
   int grid;       // persistent CTAs
   size_t off_tickets, off_part_o, off_part_l, ws_bytes;
 };
-AttnPlan plan_attention(int B, int T, int Hq, int Hkv, int D, int kv_cap, int sm_count, bool whole = false);
+AttnPlan plan_attention(int B, int T, int Hq, int Hkv, int D, int kv_cap, int sm_count, bool parts = false);
 
 struct AttnArgs {
   const void *q;
@@ -92,7 +92,6 @@ struct AttnArgs {
 // bf16 inputs, tensor cores, TMA tiles, persistent split-KV with in-kernel merge.
 cudaError_t launch_attention_tc(const AttnPlan &p, const AttnArgs &a, const CUtensorMap &kmap,
                                 const CUtensorMap &vmap);
-cudaError_t clear_attention_tickets(const AttnPlan &p, void *ws, cudaStream_t stream);
 // Any-dtype CUDA-core attention, one CTA per (sequence, KV head).
 size_t simt_attention_ws_bytes();
 cudaError_t launch_attention_simt(const AttnPlan &p, const AttnArgs &a);
@@ -119,7 +118,7 @@ struct PrefixGeom {
 // float32: the own caches in chunks of `keys`, one partial result for each (sequence, KV head, row tile) and
 // chunk; count == 0: one result a row.
 struct OwnChunks {
-  int count, keys, row_tiles, slot_rows, cap;
+  int count, keys, row_tiles, tile_rows, slot_rows, cap;
 };
 struct PrefixPlan {
   PrefixGeom g;

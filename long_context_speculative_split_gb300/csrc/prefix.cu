@@ -304,7 +304,8 @@ __global__ void __launch_bounds__(kMergeThreads)
   } else {
     const int b = bt / g.T, ro = r - b * g.T * g.G;  // row among the sequence's own
     const int n = min(own.count, (kv_len[b] + own.keys - 1) / own.keys);
-    const int64_t at = (static_cast<int64_t>(b * g.Hkv + h) * own.row_tiles + ro / kSRows) * own.count * own.slot_rows + ro % kSRows;
+    const int64_t at = (static_cast<int64_t>(b * g.Hkv + h) * own.row_tiles + ro / own.tile_rows) * own.count * own.slot_rows +
+                       ro % own.tile_rows;
     m = __ldcg(own_l + at);
     o = __ldcg(reinterpret_cast<const float4 *>(own_o + at * D + d));
     add_all(own_l, own_o, at + own.slot_rows, own.slot_rows, n - 1);
@@ -368,9 +369,11 @@ cudaError_t launch_prefix_merge(const PrefixPlan &p, const PrefixArgs &a, const 
 // clusters out of `most`: the number that by these measured rates ends both first, with the capacities in
 // place of the lengths, which only the device knows.  Prefix: 6 us, 1.8 us a step and 2 us for every
 // further pair that a cluster has a part of (none where all parts end with a pair).  Own caches: from 6 us
-// on 55 GB/s an SM; what is left when the prefix kernel ends takes 8 us (a sequence) and 6.1 TB/s.
-// Measured against all pairs of SMs for the prefix kernel and the rest after it: 39.1 to 48.6 us for 128
-// new rows on 8192 shared keys with up to 512 own keys each, 326 to 333 us for 640 rows on 32768.
+// on 55 GB/s of capacity an SM (34 GB/s of rows, at the lengths of caches that are 60 % full: with full ones
+// the prefix kernel gets more SMs than would be best); what is left when the prefix kernel ends takes 8 us
+// (a sequence) and 6.1 TB/s.  Measured against all pairs of SMs for the prefix kernel and the rest after it:
+// 38 to 48 us for 128 new rows on 8192 shared keys with up to 512 own keys each, 323 to 333 us for 640 rows
+// on 32768.
 int prefix_share(const PrefixPlan &p, int most, int sm_count) {
   const PrefixLine line = prefix_line(p.g, p.g.prefix_cap, most);
   const double own = 4.0 * p.g.B * p.g.Hkv * p.own_cap * p.g.D;  // bytes of K and V
@@ -417,6 +420,7 @@ PrefixPlan plan_prefix(int B, int T, int Hq, int Hkv, int D, int prefix_cap, int
     c.keys = ((kv_cap + 7) / 8 + kSKeys - 1) / kSKeys * kSKeys;
     c.count = (kv_cap + c.keys - 1) / c.keys;
     c.row_tiles = (T * g.G + kSRows - 1) / kSRows;
+    c.tile_rows = kSRows;
     c.slot_rows = std::min(kSRows, T * g.G);
     own_rows = static_cast<size_t>(B) * Hkv * c.row_tiles * c.count * c.slot_rows;
   }
@@ -430,6 +434,16 @@ PrefixPlan plan_prefix(int B, int T, int Hq, int Hkv, int D, int prefix_cap, int
   off = align_up(off + slots * g.slot_rows * D * sizeof(float));
   p.off_part_l = off;
   off = align_up(off + slots * g.slot_rows * sizeof(float));
+  if (!in_f32 && p.own.nchunk > 1) {  // as the attention kernel keeps them
+    OwnChunks &c = p.chunks;
+    c.cap = kv_cap;
+    c.keys = p.own.C;
+    c.count = p.own.nchunk;
+    c.row_tiles = p.own.RG;
+    c.tile_rows = c.slot_rows = 32;
+    p.off_own_o = p.own.off_part_o;
+    p.off_own_l = p.own.off_part_l;
+  }
   p.ws_bytes = off;
   return p;
 }

@@ -301,3 +301,28 @@ def test_many_small_weights_beside_a_large_one(gap, late):
     part = (P - 1) * math.exp(-gap) / (1 + (P - 1) * math.exp(-gap))
     assert (out.double() - ref).abs().max() <= 4.9e-4 / (1 + (P - 1) * math.exp(-gap)) + 1e-3 * part
     assert_lse_close(lse, ref_lse.cpu().numpy())
+
+
+@pytest.mark.parametrize("case", [
+    (2, 4, 32, 8, 128, 300, 300, [1500, 513], 1500),         # three parts of 512 keys, and two with one key
+    (3, 17, 32, 8, 64, 0, 16, [2049, 17, 1024], 2100),       # more than 32 rows a sequence, no prefix
+    (1, 2, 48, 1, 64, 100, 128, [3000], 3000),               # 96 rows of one sequence
+    (2, 1, 8, 2, 128, 64, 64, [512, 1], 5000),               # short sequences in long caches
+    (5, 3, 16, 4, 128, 1000, 1000, [20000, 16384, 16385, 3, 700], 20000),
+], ids=lambda c: "B%d_T%d_own%d" % (c[0], c[1], c[8]))
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+def test_own_caches_in_parts(case, dtype):
+    """Few sequences with long caches of their own, which are attended in parts."""
+    dev = gpu_or_skip()
+    a = _inputs(dev, *case, dtype)
+    B, T, Hq, Hkv, D, _, pcap, _, cap = case
+    need = mgd.mgd_prefix_workspace_size(B, T, Hq, Hkv, D, pcap, cap)
+    ws = Guarded((need // 4,), torch.int32, dev, init=torch.zeros(()))
+    out, lse = Guarded((B, T, Hq, D), torch.float32, dev), Guarded((B, T, Hq), torch.float32, dev)
+    ref, ref_lse = _reference(a)
+    for _ in range(2):  # the second call finds what the first one left
+        ops.prefix_attn(**a, ws=ws.t.view(torch.uint8), out=out.t, lse=lse.t)
+        torch.cuda.synchronize()
+        check_guards(ws=ws, out=out, lse=lse)
+        assert mgd.mgd_workspace_errors(ws.t) == 0
+        _check_close(out.t, lse.t, ref, ref_lse, dtype)

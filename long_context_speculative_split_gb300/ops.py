@@ -251,30 +251,34 @@ def streaming_select(k, v, kv_len, sink, K, draft_cap=None, out=None, stream=Non
     return out
 
 
-def _as_wanted(device, dense, int32, f32, same):
-    """Whether _check() would pass, without its lists of names (it is called to say what is wrong)."""
-    where, d0 = device.index, same[0].dtype if same else None
-    for t in dense:
-        if t is not None and not (t.is_contiguous() and t.get_device() == where):
-            return False
+def _as_wanted(device, int32, f32, dense, same):
+    """Whether _check() would pass, without its lists of names (it is called to say what is wrong): `int32` and
+    `f32` of that type and packed, `dense` packed, `same` of one type, all on `device`."""
+    where = device.index
     for t in int32:
-        if t is not None and t.dtype is not torch.int32:
+        if t is not None and (t.dtype is not torch.int32 or t.get_device() != where or not t.is_contiguous()):
             return False
     for t in f32:
-        if t is not None and t.dtype is not torch.float32:
+        if t.dtype is not torch.float32 or t.get_device() != where or not t.is_contiguous():
             return False
+    for t in dense:
+        if t.get_device() != where or not t.is_contiguous():
+            return False
+    first = same[0].dtype
     for t in same:
-        if t.dtype is not d0 or t.get_device() != where:
+        if t.dtype is not first or t.get_device() != where:
             return False
     return True
 
 
-def _on_current(device):
-    """The launch goes to the current device: refuse tensors of another one, or of the host."""
-    if device.index is None:
+def _launch_stream(device, stream):
+    """The stream of a launch.  It goes to the current device: refuse tensors of another one, or of the host."""
+    index = device.index
+    if index is None:
         raise ValueError("the tensors are on %s: a CUDA device is needed" % device)
-    if device.index != torch.cuda.current_device():
+    if index != torch.cuda.current_device():
         raise ValueError("the tensors are on %s, the current device is cuda:%d" % (device, torch.cuda.current_device()))
+    return torch._C._cuda_getCurrentRawStream(index) if stream is None else stream
 
 
 def prefix_attn(q, k_prefix, v_prefix, prefix_len, k, v, kv_len, sm_scale=None, out_dtype=torch.float32, ws=None,
@@ -306,13 +310,13 @@ def prefix_attn(q, k_prefix, v_prefix, prefix_len, k, v, kv_len, sm_scale=None, 
         lse = torch.empty(shape[:-1], dtype=torch.float32, device=dev)
     if out.shape != shape or lse.shape != shape[:-1]:
         raise ValueError("out must have q's shape and lse the same without D")
-    if not _as_wanted(dev, (q, kv_len, prefix_len, out, lse), (kv_len, prefix_len), (lse,), (q, k_prefix, v_prefix, k, v)):
+    if not _as_wanted(dev, (kv_len, prefix_len), (lse,), (q, out), (q, k_prefix, v_prefix, k, v)):
         _check(dev, dense=[("q", q), ("kv_len", kv_len), ("prefix_len", prefix_len), ("out", out), ("lse", lse)],
                int32=[("kv_len", kv_len), ("prefix_len", prefix_len)], f32=[("lse", lse)],
                same=[("q", q), ("k_prefix", k_prefix), ("v_prefix", v_prefix), ("k", k), ("v", v)])
     if ws is None:
         ws = workspace(mgd.mgd_prefix_workspace_size(B, T, Hq, Hkv, D, pshape[1], cap), dev)
-    _on_current(dev)
+    stream = _launch_stream(dev, stream)
     mgd.mgd_prefix_attn(q, k_prefix, v_prefix, prefix_len, pshape[1], ps[0], k, v, kv_len, B, T, Hq, Hkv, D, cap, sb, sh,
                         scale, _dtype_code(q), out, _dtype_code(out), lse, ws, ws.numel(), stream)
     return out, lse
@@ -371,9 +375,14 @@ def rope_append(q, k_new, v_new, table, k, v, kv_len, new_len=None, pos_offset=N
     Hkv, cap = kshape[1], kshape[2]
     if kshape[0] != B or kshape[3] != D or v.shape != kshape or kv_len.numel() != B:
         raise ValueError("k, v must be [B, Hkv, kv_cap, D] and kv_len [B]")
-    sq = _token_stride("q", q, B, T, Hq, D)
-    sk = _token_stride("k_new", k_new, B, T, Hkv, D)
-    sv = _token_stride("v_new", v_new, B, T, Hkv, D)
+    s, nshape = q.stride(), k_new.shape
+    if (T > 1 and s[3] == 1 and s[2] == D and s[0] == T * s[1] and nshape == (B, T, Hkv, D) and v_new.shape == nshape
+            and k_new.stride() == s and v_new.stride() == s):
+        sq = sk = sv = s[1]  # views of one fused projection
+    else:
+        sq = _token_stride("q", q, B, T, Hq, D)
+        sk = _token_stride("k_new", k_new, B, T, Hkv, D)
+        sv = _token_stride("v_new", v_new, B, T, Hkv, D)
     sb, sh = _kv_strides(k, v, D)
     if new_len is not None and new_len.numel() != B:
         raise ValueError("new_len must be [B]")
@@ -386,15 +395,14 @@ def rope_append(q, k_new, v_new, table, k, v, kv_len, new_len=None, pos_offset=N
         raise ValueError("q_out must have q's shape")
     if turns.dtype is not torch.int64 or turns.numel() != table.rotary_dim // 2:
         raise TypeError("table must come from rope_table")
-    if not _as_wanted(dev, (kv_len, new_len, pos_offset, q_out, turns), (kv_len, new_len, pos_offset), (),
-                      (q, k_new, v_new, k, v, q_out)):
+    if not _as_wanted(dev, (kv_len, new_len, pos_offset), (), (q_out, turns), (q, k_new, v_new, k, v, q_out)):
         _check(dev, dense=[("kv_len", kv_len), ("new_len", new_len), ("pos_offset", pos_offset), ("q_out", q_out),
                            ("table", turns)],
                int32=[("kv_len", kv_len), ("new_len", new_len), ("pos_offset", pos_offset)],
                same=[("q", q), ("k_new", k_new), ("v_new", v_new), ("k", k), ("v", v), ("q_out", q_out)])
     if ws is None:
         ws = workspace(mgd.mgd_rope_workspace_size(B), dev)
-    _on_current(dev)
+    stream = _launch_stream(dev, stream)
     mgd.mgd_rope_append(q, sq, k_new, sk, v_new, sv, turns, table.magnitude, table.rotary_dim, int(interleaved), B, T, Hq,
                         Hkv, D, _dtype_code(q), kv_len, new_len, pos_offset, 1 if offsets > 1 else 0, q_out, k, v, cap, sb,
                         sh, ws, ws.numel(), stream)
@@ -430,15 +438,14 @@ def token_logprobs(logits, tokens, top=0, ws=None, out=None, stream=None):
     for name, want in (("logprob", lead), ("entropy", lead), ("rank", lead), ("top_ids", tops), ("top_logprobs", tops)):
         if out[name].shape != want:
             raise ValueError("out[%r] has the wrong shape" % name)
-    if not _as_wanted(dev, (tokens, logprob, entropy, rank, ids, lps), (tokens, rank, ids), (logprob, entropy, lps),
-                      (logits,)):
+    if not _as_wanted(dev, (tokens, rank, ids), (logprob, entropy, lps), (), (logits,)):
         ints = [("tokens", tokens), ("rank", rank), ("top_ids", ids)]
         floats = [("logprob", logprob), ("entropy", entropy), ("top_logprobs", lps)]
         _check(dev, dense=ints + floats, int32=ints, f32=floats)
     if ws is None:
         ws = workspace(mgd.mgd_logprobs_workspace_size(R, V, top), dev)
     code = _dtype_code(logits)
-    _on_current(dev)
+    stream = _launch_stream(dev, stream)
     mgd.mgd_token_logprobs(logits, step or V, code, tokens, R, V, top, logprob, entropy, rank, ids, lps, ws,
                            ws.numel(), stream)
     return out

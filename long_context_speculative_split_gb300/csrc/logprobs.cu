@@ -23,7 +23,7 @@
 //
 // Measured at V = 128256: 2048 bfloat16 rows with 20 alternatives 132 us, 4.0 TB/s (choosing
 // in every block: 164 us; without the choice: about 120 us; two CTAs of 384 threads an SM: 154 us,
-// five of 128: 137 us); 384 float32 rows of 640 with 8 alternatives 42 us, 4.7 TB/s; 4 rows 10.6 us.
+// five of 128: 137 us); 384 float32 rows of 640 with 8 alternatives 43 us, 4.6 TB/s; 4 rows 11 us.
 #include <algorithm>
 
 #include "common.cuh"
@@ -258,6 +258,7 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas)
     sh.gave_up = 0;
   }
   __syncthreads();
+  if (C > 1) cluster_arrive_relaxed();  // waited for before the first write to another CTA's shared memory
   // rows without a token
   for (int64_t i = (static_cast<int64_t>(blockIdx.y) * C + part) * kLpThreads + tid; i < R;
        i += static_cast<int64_t>(gridDim.y) * C * kLpThreads) {
@@ -559,6 +560,7 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas)
       }
     }
     // ---- this CTA's part
+    if (C > 1 && done == 0) cluster_wait();
     warp_fold(me);
     if (lane == 0) sh.warp[warp] = me;
     __syncthreads();
@@ -616,6 +618,7 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas)
     }
     if (C > 1) cluster_sync_all();  // the next row's parts come after this one's have been read
   }
+  if (C > 1 && done == 0) cluster_wait();
   if (tid == 0 && sh.gave_up) atomicOr(&hdr->err[0], 0x8u);  // (2 s after the call's bits were written)
 }
 
@@ -623,7 +626,7 @@ template <typename Tin>
 cudaError_t logprobs_one(const LogprobArgs &a) {
   // CTAs a row: as many as the row has work for, up to 8, as long as there are not rows enough to go
   // round without: meeting costs a cluster about 3 us a row (640 rows of 128256 float32: 86 us by fours,
-  // 48 us by one; 4 rows: 10.7 us by eights, 30 us by one).
+  // 48 us by one, of an earlier form; 4 rows: 11 us by eights, 30 us by one).
   const int slots = kLpCtas * current_sm_count();
   int C = 1;
   while (C < kLpMaxCluster && a.V > C * kLpThreads * kLpLoads * 2 && static_cast<int64_t>(a.R) * C < slots) C *= 2;

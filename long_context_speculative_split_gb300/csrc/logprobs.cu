@@ -624,14 +624,15 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas)
 
 template <typename Tin>
 cudaError_t logprobs_one(const LogprobArgs &a) {
-  // CTAs a row: as many as it has blocks for, up to 8, as long as there are not rows enough to go round
-  // without, since meeting costs a cluster about 3 us a row.  384 float32 rows of 128256: 43 us by one, 49 by
-  // twos, 80 by fours; 4 of them: 27 us by one, 12.2 by fours, 11.0 by eights; 37 bfloat16 rows of 50257:
-  // 11.6 us by one, 9.1 by fours, 10.0 by eights.
+  // CTAs a row: as many as it has blocks for, up to 8, as long as all rows are taken at once: meeting
+  // costs a cluster about 3 us a row.  384 float32 rows of 128256: 43 us by one, 49 by twos, 80 by fours; 4 of
+  // them: 27 us by one, 12.2 by fours, 11.0 by eights; 100 bfloat16 rows of 128256: 13.2 us by fours, 21.7 by
+  // eights that take some rows in a second turn; 37 bfloat16 rows of 50257: 11.6 us by one, 9.0 by fours,
+  // 10.0 by eights.
   const int slots = kLpCtas * current_sm_count();
   const int64_t chunks = static_cast<int64_t>(a.V) * sizeof(Tin) / 16;
   int C = 1;
-  while (C < kLpMaxCluster && chunks > C * kLpChunks && static_cast<int64_t>(a.R) * C < slots) C *= 2;
+  while (C < kLpMaxCluster && chunks > C * kLpChunks && 2LL * a.R * C <= slots) C *= 2;
   constexpr int smem = kLpStages * kLpStageBytes;
   cudaError_t e = want_shared_memory<logprobs_kernel<Tin>>(smem);
   if (e != cudaSuccess) return e;

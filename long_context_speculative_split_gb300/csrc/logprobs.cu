@@ -18,8 +18,8 @@
 // value, the K-th largest of these values bounds the K-th best entry from below, so a handful more
 // than K of the threads' parts of blocks hold an entry at or above it.  Only those are looked at
 // again, and what they have above the bound is put in order.  (Where ties or sorted rows leave more
-// than the lists hold, the CTA takes the maximum K times.)  The parts meet in the first CTA's shared
-// memory.
+// than the lists hold, the CTA goes through those blocks entry by entry.)  The parts meet in the first
+// CTA's shared memory.
 //
 // Measured at V = 128256: 2048 bfloat16 rows with 20 alternatives 132 us, 4.0 TB/s (choosing
 // in every block: 164 us; without the choice: about 120 us; two CTAs of 384 threads an SM: 154 us,
@@ -74,7 +74,6 @@ struct RowPart {
 struct LpShared {
   unsigned long long list[kLpList + 2];         // entries put aside
   unsigned long long best[kLpMaxK];             // the best so far, in order
-  unsigned long long red[kLpThreads / 32];
   unsigned long long all[kLpMaxCluster][kLpMaxK];  // of every CTA, in the first one's shared memory
   RowPart part[kLpMaxCluster];
   RowPart warp[kLpThreads / 32];
@@ -128,6 +127,9 @@ struct Entries<float> {
     }
     return fmax3_nan(m[0], m[1], m[1]);
   }
+  static __device__ __forceinline__ float largest(const uint4 &c) {
+    return fmaxf(fmaxf(__uint_as_float(c.x), __uint_as_float(c.y)), fmaxf(__uint_as_float(c.z), __uint_as_float(c.w)));
+  }
   // entries above a threshold, summed over the chunks of a block: ones and sums as floats, two at a time
   struct Count {
     float2 n = make_float2(0.f, 0.f);
@@ -161,6 +163,10 @@ struct Entries<__nv_bfloat16> {
     }
     const float2 a = __bfloat1622float2(__hmax2_nan(m[0], m[1]));
     return fmax3_nan(a.x, a.y, a.y);
+  }
+  static __device__ __forceinline__ float largest(const uint4 &c) {
+    const float2 a = __bfloat1622float2(__hmax2(__hmax2(two(c.x), two(c.y)), __hmax2(two(c.z), two(c.w))));
+    return fmaxf(a.x, a.y);
   }
   // in pairs of bfloat16: the threshold is a bfloat16 value, and a block's count, at most 32 in either
   // half, is exact in bfloat16
@@ -521,33 +527,53 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas)
         }
         __syncthreads();
         if (hits > kLpHits || sh.count > kLpList) {
-          // more than the lists hold: the largest key below the last one, K times, of this span and of what
-          // the list had before it (entries of this span that are in the list count once: keys are unique)
-          unsigned long long last = ~0ull;
-          for (int k = 0; k < K; ++k) {
-            unsigned long long b = 0;
-            auto see = [&](unsigned long long key) {
-              if (key < last && key > b) b = key;
-            };
-            for (int i = tid; i < min(sh.count, kLpList); i += kLpThreads) see(sh.list[i]);
-            const int e1 = head + min(span + kLpSpan * kLpChunks, c1) * VE;
-            for (int j = head + span * VE + tid; j < e1; j += kLpThreads) {
-              const float v = to_f32(x0[j]);
-              if (v > -INFINITY) see(order_key(v, j));
-            }
-            if (edge >= 0 && span == c0 && ex > -INFINITY) see(order_key(ex, edge));
-            for (int o = 16; o; o >>= 1) {
-              const unsigned long long y = __shfl_xor_sync(0xffffffffu, b, o);
-              b = y > b ? y : b;
-            }
-            if (lane == 0) sh.red[warp] = b;
+          // More than the lists hold (ties, or the best entries all in few threads' parts): the span once more,
+          // against the bound and then the K-th best key so far, in steps that the list has room for.  With
+          // ties that key is soon one of the lowest indices, and the steps without a better one are passed
+          // over.  640 float32 rows of 128256 with all but 10 entries masked by the lowest value: 217 us,
+          // 81 us unmasked; with the largest entry taken K times instead, 1.9 ms.
+          int n = span == c0 ? 0 : K;  // entries in the list: the best of the spans before
+          __syncthreads();             // every thread has read the count
+          if (tid == 0) sh.count = n;
+          __syncthreads();
+          unsigned long long bar = n ? sh.list[K - 1] : 0;
+          if (floor > -INFINITY) bar = max(bar, order_key(floor, 0xFFFFFFFFu));  // just below the keys of that value
+          auto key_of = [&](float v, int j) { return v > -INFINITY ? order_key(v, j) : 0ull; };
+          auto put = [&](unsigned long long key) {  // every thread, a key or 0
+            const bool better = key > bar;
+            if (better) sh.list[atomicAdd(&sh.count, 1)] = key;
+            n += __syncthreads_count(better);
+            if (n <= kLpList - kLpThreads / 2) return;
+            put_in_order(sh.list, n, sh.best, K);
+            if (tid < K) sh.list[tid] = sh.best[tid];
+            if (tid == 0) sh.count = K;
+            n = K;
+            bar = sh.best[K - 1];
             __syncthreads();
-            b = 0;
-            for (int i = 0; i < kLpThreads / 32; ++i) b = sh.red[i] > b ? sh.red[i] : b;
-            if (tid == 0) sh.best[k] = b;
-            last = b;
-            __syncthreads();
+          };
+          put(edge >= 0 && span == c0 ? key_of(ex, edge) : 0);
+          const int span_end = min(span + kLpSpan * kLpChunks, c1);
+          for (int base = span; base < span_end; base += 2 * kLpThreads) {
+            uint4 x[2];
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+              const int c = base + u * kLpThreads + tid;
+              x[u] = c < span_end ? __ldg(reinterpret_cast<const uint4 *>(x0 + head) + c) : En::none();
+            }
+            bool any = false;
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+              any |= key_of(En::largest(x[u]), head + (base + u * kLpThreads + tid) * VE) > bar;
+            if (!__syncthreads_or(any)) continue;
+#pragma unroll 1
+            for (int h = 0; h < 4 * VE; ++h) {  // the entries of half the threads' chunks at a time
+              const int c = base + (h & 1) * kLpThreads + tid, e = h >> 2;
+              const bool mine = (tid >= kLpThreads / 2) == (h >> 1 & 1) && c < span_end;
+              const int j = head + c * VE + e;
+              put(mine ? key_of(to_f32(x0[j]), j) : 0);
+            }
           }
+          put_in_order(sh.list, n, sh.best, K);
         } else {
           put_in_order(sh.list, sh.count, sh.best, K);
         }

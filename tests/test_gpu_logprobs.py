@@ -221,3 +221,22 @@ def test_rows_far_from_zero(dtype):
     out, err = _run(x, tok, K)
     assert err == 0
     _check(x, tok, K, out)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("R", [3, 460])
+def test_fewer_entries_allowed_than_alternatives(R, dtype):
+    """All but a few entries masked by the type's lowest value: the rest of the alternatives are masked
+    entries, the lowest indices first, over rows that begin at odd addresses."""
+    dev = gpu_or_skip()
+    V, K = 70003, 32
+    x = torch.full((R, V), torch.finfo(dtype).min, dtype=dtype, device=dev)
+    for i, at in enumerate((0, 1, 5, 4095, 40000, V - 1)):
+        x[:, at] = i - 3
+    x[1::3, :64] = -1.0  # ties above the mask, more than the alternatives
+    x[2::3, -50:] = 2.5  # at the row's end
+    tok = torch.arange(R, device=dev).to(torch.int32) % 7
+    out, err = _run(x, tok, K)
+    assert err == 0
+    few = [*range(min(R, 9))] + ([] if R < 20 else [R - 2, R - 1])
+    _check(x[few], tok[few], K, {n: t[few] for n, t in out.items()})
